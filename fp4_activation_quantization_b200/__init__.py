@@ -13,7 +13,9 @@ Functions carry the C names:
 ``nq_fused_add_rmsnorm_quant_fp8``, ``nq_rmsnorm_quant_fp8_static``,
 ``nq_layernorm_quant_fp8``, ``nq_per_token_group_quant_fp8``,
 ``nq_rmsnorm_quant_nvfp4``, ``nq_rmsnorm_quant_fp8_group``; plus
-``nq_query_schedule``.
+``nq_query_schedule``.  The 4-bit key/value cache: ``nq_kv_plan``,
+``nq_kv_append_nvfp4``, ``nq_kv_gather_nvfp4``, ``nq_attention_nvfp4_kv`` and
+``kv_cache_shape``.
 """
 from __future__ import annotations
 
@@ -32,6 +34,8 @@ __all__ = [
     "OP_RMS_DYN_FP8", "OP_RMS_STATIC_FP8", "OP_LN_STATIC_FP8", "OP_RMS_NVFP4", "OP_RMS_GROUP_FP8",
     "nq_rmsnorm_quant_fp8_group", "nq_check_device_errors", "nq_selftest_division",
     "nq_fused_add_rmsnorm_quant_fp8_moe",
+    "FLAG_NONCAUSAL", "NQ_KV_MAX_REQUESTS", "ATTENTION_WORKSPACE_BYTES", "kv_cache_shape", "nq_kv_plan",
+    "nq_kv_append_nvfp4", "nq_kv_gather_nvfp4", "nq_attention_nvfp4_kv",
 ]
 
 NQ_OK, NQ_ERR_INVALID_ARGUMENT, NQ_ERR_UNSUPPORTED, NQ_ERR_CUDA = 0, 1, 2, 3
@@ -45,6 +49,9 @@ FLAG_E5M2 = 1 << 5
 FLAG_SF_SWIZZLED = 1 << 6
 FLAG_SCALES_COL_MAJOR = 1 << 7
 FLAG_SCALES_PACKED_UE8M0 = 1 << 8
+FLAG_NONCAUSAL = 1 << 9
+NQ_KV_MAX_REQUESTS = 16384
+ATTENTION_WORKSPACE_BYTES = 32 << 20
 OP_RMS_DYN_FP8, OP_RMS_STATIC_FP8, OP_LN_STATIC_FP8, OP_RMS_NVFP4, OP_RMS_GROUP_FP8 = 0, 1, 2, 3, 4
 
 
@@ -97,6 +104,14 @@ def _load() -> ctypes.CDLL:
     L.nq_rmsnorm_quant_nvfp4.argtypes = [P, I64, P, P, I64, P, P, P, I64, P, I64, P, I64, I64, I64, F, U32, P]
     L.nq_fused_add_rmsnorm_quant_fp8_moe.argtypes = [P, I64, P, P, I64, P, P, I32, I64, P, I64, P, I64, P, I64,
                                                      I64, I64, I32, F, U32, P]
+    L.nq_kv_page_bytes.argtypes, L.nq_kv_page_bytes.restype = [I32, I32, I32], I64
+    L.nq_kv_plan.argtypes = [P, P, P, I64, I32, P, I64, P, P, P, P, P, P, I64, I64, I32, U32, P]
+    L.nq_kv_append_nvfp4.argtypes = [P, I64, I64, P, I64, I64, P, P, P, P, I64, I64, I64, I32, I32, I32, U32, P]
+    L.nq_kv_gather_nvfp4.argtypes = [P, I64, I64, P, P, P, P, I64, I64, P, I64, I64, I64, I32, I32, I32, U32, P]
+    L.nq_attention_nvfp4_kv.argtypes = [P, I64, I64, P, I64, I64, P, I64, I32, P, P, P, P, P, I64, I64, P, I64, P, I64,
+                                        I64, I64, I32, I32, I32, I32, F, I32, U32, P]
+    for name in ("nq_kv_plan", "nq_kv_append_nvfp4", "nq_kv_gather_nvfp4", "nq_attention_nvfp4_kv"):
+        getattr(L, name).restype = st
     for name in ("nq_fused_add_rmsnorm_quant_fp8", "nq_rmsnorm_quant_fp8_static", "nq_layernorm_quant_fp8",
                  "nq_per_token_group_quant_fp8", "nq_rmsnorm_quant_nvfp4", "nq_rmsnorm_quant_fp8_group",
                  "nq_fused_add_rmsnorm_quant_fp8_moe"):
@@ -483,3 +498,180 @@ def nq_fused_add_rmsnorm_quant_fp8_moe(x, gamma, dest, rows: int, eps: float = 1
             _ptr(q_out), ld_q, _ptr(scales_out), ld_s, _ptr(norm_out), ld_n, M, d, group, eps, flags,
             _stream(stream)), "nq_fused_add_rmsnorm_quant_fp8_moe")
     return q_out, scales_out, residual_out, norm_out
+
+
+# ------------------------------------------------- the 4-bit key/value cache ----
+def kv_cache_shape(num_pages: int, kv_heads: int, head_dim: int, page_size: int):
+    """Shape of a uint8 cache tensor: [pages, kv heads, page_size * head_dim * 9 / 8]."""
+    return num_pages, kv_heads, page_size * head_dim * 9 // 8
+
+
+def _launch(device, name, *args, stream=None) -> None:
+    """Call ``name`` on ``device``, the stream last; the device context is entered only when it is another one."""
+    index = device.index
+    if index is None or index == torch.cuda.current_device():
+        status = getattr(_get_lib(), name)(*args, _stream(stream))
+    else:
+        with torch.cuda.device(device):
+            status = getattr(_get_lib(), name)(*args, _stream(stream))
+    if status != NQ_OK:
+        raise NQError(status, name)
+
+
+def _ints(t, name: str, dtype, n: int):
+    _need(isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == dtype and t.shape == (n,)
+          and (n <= 1 or t.stride(0) == 1), f"{name} must be a contiguous {dtype} CUDA tensor [{n}]")
+
+
+def _heads(t, name: str, d: int | None = None, heads: int | None = None):
+    """bf16 [T, heads, d] on CUDA, last dimension contiguous: (T, heads, d, token stride, head stride)."""
+    _need(isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == torch.bfloat16 and t.dim() == 3,
+          f"{name} must be a bfloat16 CUDA tensor [T, heads, d]")
+    T, H, D = t.shape
+    s0, s1, s2 = t.stride()
+    _need(s2 == 1, f"{name} must have a contiguous last dimension")
+    _need((d is None or D == d) and (heads is None or H == heads), f"{name} must be [T, {heads}, {d}], got {(T, H, D)}")
+    if H <= 1:
+        s1 = max(s1, D)
+    if T <= 1:
+        s0 = max(s0, H * D if s1 <= D else (H - 1) * s1 + D)
+    return T, H, D, s0, s1
+
+
+def _cache(cache, d: int):
+    """(pages, kv heads, tokens a page, page stride) of a cache tensor for head dimension d."""
+    _need(isinstance(cache, torch.Tensor) and cache.is_cuda and cache.dtype == torch.uint8 and cache.dim() == 3,
+          "cache must be a uint8 CUDA tensor of kv_cache_shape")
+    pages, heads, n = cache.shape
+    s0, s1, s2 = cache.stride()
+    _need(s2 == 1 and (heads <= 1 or s1 == n), "cache must be contiguous within a page")
+    _need(d > 0 and n * 8 % (9 * d) == 0, f"cache rows of {n} bytes hold no whole tokens of head dimension {d}")
+    return pages, heads, n * 8 // (9 * d), (s0 if pages > 1 else max(s0, heads * n))
+
+
+def _table(block_table, B: int):
+    _need(isinstance(block_table, torch.Tensor) and block_table.is_cuda and block_table.dtype == torch.int32
+          and block_table.dim() == 2 and block_table.shape[0] == B, f"block_table must be an int32 CUDA tensor [{B}, pages]")
+    width = block_table.shape[1]
+    _need(width <= 1 or block_table.stride(1) == 1, "block_table must have a contiguous last dimension")
+    return width, (block_table.stride(0) if B > 1 else max(block_table.stride(0), width))
+
+
+def nq_kv_plan(cached_lens, new_lens, block_table, free_pages, free_head, tokens: int, page_size: int, *,
+               free_head_out=None, flags: int = 0, stream=None):
+    """Block table rows, slots and positions of a step's tokens from the requests' lengths.
+
+    ``cached_lens``, ``new_lens`` int32 [B]; ``block_table`` int32 [B, pages],
+    the new pages' columns are filled in place; ``free_pages`` int32, taken from
+    entry ``free_head`` (int32 [1]) on; ``tokens`` rows are produced, those
+    behind the last token hold -1.  Returns ``(cu_q int32 [B + 1], kv_lens int32
+    [B], positions int32 [tokens], slots int64 [tokens], free_head_out int32
+    [1])``; pass ``free_head_out=free_head`` to advance the list in place.
+    """
+    _need(isinstance(new_lens, torch.Tensor) and new_lens.dim() == 1, "new_lens must be an int32 CUDA tensor [B]")
+    B, dev = new_lens.shape[0], new_lens.device
+    _ints(cached_lens, "cached_lens", torch.int32, B)
+    _ints(new_lens, "new_lens", torch.int32, B)
+    width, ld = _table(block_table, B)
+    _need(isinstance(free_pages, torch.Tensor) and free_pages.dim() == 1, "free_pages must be an int32 CUDA tensor")
+    _ints(free_pages, "free_pages", torch.int32, free_pages.shape[0])
+    _ints(free_head, "free_head", torch.int32, 1)
+    _need(tokens >= 0, "tokens must not be negative")
+    if free_head_out is None:
+        free_head_out = torch.empty(1, dtype=torch.int32, device=dev)
+    _ints(free_head_out, "free_head_out", torch.int32, 1)
+    _same_device(cached_lens, new_lens, block_table, free_pages, free_head, free_head_out)
+    cu_q = torch.empty(B + 1, dtype=torch.int32, device=dev)
+    kv_lens = torch.empty(B, dtype=torch.int32, device=dev)
+    positions = torch.empty(tokens, dtype=torch.int32, device=dev)
+    slots = torch.empty(tokens, dtype=torch.int64, device=dev)
+    _launch(dev, "nq_kv_plan", cached_lens.data_ptr(), new_lens.data_ptr(), block_table.data_ptr(), ld, width,
+            free_pages.data_ptr(), free_pages.shape[0], free_head.data_ptr(), free_head_out.data_ptr(), cu_q.data_ptr(),
+            kv_lens.data_ptr(), positions.data_ptr(), slots.data_ptr(), B, tokens, page_size, flags, stream=stream)
+    return cu_q, kv_lens, positions, slots, free_head_out
+
+
+def nq_kv_append_nvfp4(k, v, slots, cache, k_scale, v_scale, *, flags: int = 0, stream=None) -> None:
+    """Quantize keys and values (bf16 [T, kv heads, d], any token and head strides) into
+    their slots (int64 [T], < 0 skips) of ``cache`` (uint8 of ``kv_cache_shape``), under
+    the one-element float32 global scales ``k_scale`` and ``v_scale``."""
+    T, H, d, kt, kh = _heads(k, "k")
+    Tv, _, _, vt, vh = _heads(v, "v", d, H)
+    _need(Tv == T, f"v must have {T} tokens")
+    pages, heads, page, stride = _cache(cache, d)
+    _need(heads == H, f"cache has {heads} kv heads, k has {H}")
+    _ints(slots, "slots", torch.int64, T)
+    _scalar(k_scale, "k_scale")
+    _scalar(v_scale, "v_scale")
+    _same_device(k, v, slots, cache, k_scale, v_scale)
+    _launch(k.device, "nq_kv_append_nvfp4", k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, slots.data_ptr(),
+            k_scale.data_ptr(), v_scale.data_ptr(), cache.data_ptr(), stride, pages, T, H, d, page, flags, stream=stream)
+
+
+def nq_kv_gather_nvfp4(cache, slots, k_scale, v_scale, head_dim: int, *, k_out=None, v_out=None, flags: int = 0,
+                       stream=None):
+    """Read tokens back: ``(k, v)`` bf16 [T, kv heads, head_dim] of ``slots`` (int64 [T], < 0 gives zeros)."""
+    pages, H, page, stride = _cache(cache, head_dim)
+    _need(isinstance(slots, torch.Tensor) and slots.dim() == 1, "slots must be an int64 CUDA tensor [T]")
+    T = slots.shape[0]
+    _ints(slots, "slots", torch.int64, T)
+    _scalar(k_scale, "k_scale")
+    _scalar(v_scale, "v_scale")
+    k_out = _out(k_out, (T, H, head_dim), torch.bfloat16, cache, "k_out")
+    v_out = _out(v_out, (T, H, head_dim), torch.bfloat16, cache, "v_out")
+    _, _, _, kt, kh = _heads(k_out, "k_out")
+    _, _, _, vt, vh = _heads(v_out, "v_out")
+    _same_device(cache, slots, k_scale, v_scale, k_out, v_out)
+    _launch(cache.device, "nq_kv_gather_nvfp4", cache.data_ptr(), stride, pages, slots.data_ptr(), k_scale.data_ptr(),
+            v_scale.data_ptr(), k_out.data_ptr(), kt, kh, v_out.data_ptr(), vt, vh, T, H, head_dim, page, flags,
+            stream=stream)
+    return k_out, v_out
+
+
+def nq_attention_nvfp4_kv(q, cache, block_table, kv_lens, cu_q, k_scale, v_scale, *, scale: float | None = None,
+                          window: int = 0, out=None, lse=None, want_lse: bool = False, workspace=None, flags: int = 0,
+                          stream=None):
+    """Attention of a ragged batch over the 4-bit cache: prompts, chunks, single tokens, mixed.
+
+    ``q`` bf16 [T, heads, d]; request b owns rows ``cu_q[b]`` ... ``cu_q[b + 1] - 1``
+    (int32 [B + 1]), the last ones of its ``kv_lens[b]`` tokens (int32 [B]), whose
+    pages ``block_table`` (int32 [B, pages]) lists.  Causal unless ``flags`` has
+    FLAG_NONCAUSAL; ``window`` > 0 limits a row to its last ``window`` keys;
+    ``scale`` defaults to d ** -0.5.  ``workspace``: a zero-filled uint8 CUDA
+    tensor of ATTENTION_WORKSPACE_BYTES, kept between calls (one per stream);
+    without it each call makes its own.  Returns ``(out bf16 [T, heads, d], lse
+    float32 [T, heads] or None)``; rows no request owns are left as they were.
+    """
+    T, heads, d, qt, qh = _heads(q, "q")
+    pages, H, page, stride = _cache(cache, d)
+    _need(isinstance(kv_lens, torch.Tensor) and kv_lens.dim() == 1, "kv_lens must be an int32 CUDA tensor [B]")
+    B = kv_lens.shape[0]
+    _ints(kv_lens, "kv_lens", torch.int32, B)
+    _ints(cu_q, "cu_q", torch.int32, B + 1)
+    width, ld = _table(block_table, B)
+    _scalar(k_scale, "k_scale")
+    _scalar(v_scale, "v_scale")
+    if out is None:
+        out = torch.empty((T, heads, d), dtype=torch.bfloat16, device=q.device)
+        ot, oh = heads * d, d
+    else:
+        To, _, _, ot, oh = _heads(out, "out", d, heads)
+        _need(To == T, f"out must have {T} tokens")
+    if want_lse and lse is None:
+        lse = torch.empty((T, heads), dtype=torch.float32, device=q.device)
+    ld_lse = heads
+    if lse is not None:
+        _need(isinstance(lse, torch.Tensor) and lse.is_cuda and lse.dtype == torch.float32 and lse.shape == (T, heads)
+              and (heads <= 1 or lse.stride(1) == 1), f"lse must be a float32 CUDA tensor {(T, heads)}")
+        ld_lse = lse.stride(0) if T > 1 else max(lse.stride(0), heads)
+    if workspace is None:
+        workspace = torch.zeros(ATTENTION_WORKSPACE_BYTES, dtype=torch.uint8, device=q.device)
+    _need(isinstance(workspace, torch.Tensor) and workspace.is_cuda and workspace.dtype == torch.uint8
+          and workspace.dim() == 1 and (workspace.shape[0] <= 1 or workspace.stride(0) == 1),
+          "workspace must be a contiguous uint8 CUDA tensor")
+    _same_device(q, cache, block_table, kv_lens, cu_q, k_scale, v_scale, out, lse, workspace)
+    _launch(q.device, "nq_attention_nvfp4_kv", q.data_ptr(), qt, qh, cache.data_ptr(), stride, pages,
+            block_table.data_ptr(), ld, width, kv_lens.data_ptr(), cu_q.data_ptr(), k_scale.data_ptr(),
+            v_scale.data_ptr(), out.data_ptr(), ot, oh, _ptr(lse), ld_lse, workspace.data_ptr(), workspace.shape[0], T, B,
+            heads, H, d, page, d ** -0.5 if scale is None else scale, window, flags, stream=stream)
+    return out, lse

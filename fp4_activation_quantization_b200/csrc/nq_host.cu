@@ -13,11 +13,12 @@
 
 #include "nq.h"
 #include "nq_device.cuh"
+#include "nq_host.h"
 #include "nq_internal.h"
 
 // Device error word of this library: bit 1 is set by a MoE dispatch whose
-// destination row was out of range (read and cleared by
-// nq_check_device_errors).  A symbol, not an allocation; one per device.
+// destination row was out of range, bits 2 and 3 by the key/value cache calls
+// (nq_kv.h); read and cleared by nq_check_device_errors.  A symbol, not an allocation; one per device.
 __device__ uint32_t g_nq_device_error;
 // Where take_error_word leaves the word it cleared, for the host to read.
 __device__ uint32_t g_nq_device_error_taken;
@@ -526,6 +527,27 @@ bool vec_bf16(const void* p, int64_t ld) { return p == nullptr || (aligned(p, 16
 
 }  // namespace
 
+// The helpers above for the library's other host translation units.
+namespace nq {
+namespace host {
+nq_status error(nq_status st, const char* fmt, ...) {
+  char buf[512];
+  va_list ap;
+  va_start(ap, fmt);
+  std::vsnprintf(buf, sizeof(buf), fmt, ap);
+  va_end(ap);
+  return fail(st, "%s", buf);
+}
+nq_status launch(const char* fn, const void* kernel, unsigned grid, unsigned block, size_t smem, void** args, bool pdl,
+                 cudaStream_t stream) {
+  return ::launch(fn, kernel, grid, block, smem, args, pdl, stream);
+}
+uint32_t* error_word() { return device_error_word(); }
+bool allow_smem(const void* kernel, size_t bytes) { return ::allow_smem(kernel, bytes); }
+int64_t resident_ctas(const void* kernel, int block, size_t smem) { return ::resident_ctas(kernel, block, smem); }
+}  // namespace host
+}  // namespace nq
+
 extern "C" {
 
 int nq_version(void) { return 100; }
@@ -585,7 +607,8 @@ nq_status nq_check_device_errors(void) {
   }
   if (word == 0) return NQ_OK;
   return fail(NQ_ERR_CUDA, "%s: device error word 0x%x (bit 1: a MoE destination row was out of range; its "
-              "store was skipped)", fn, word);
+              "store was skipped; bit 2: a slot or page outside the key/value cache; bit 3: a key/value plan ran out "
+              "of pages, table columns or token rows)", fn, word);
 }
 
 nq_status nq_query_schedule(int op, int64_t M, int64_t d, uint32_t flags, int* threads_per_row,

@@ -1,0 +1,96 @@
+// nq_kv.h — argument blocks of the 4-bit key/value cache calls, shared by their
+// host launcher (nq_kv_host.cu) and their kernels.  Not installed.
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+
+#include "nq.h"
+
+namespace nq {
+
+// Bits of the device error word that these kernels set (read and cleared by
+// nq_check_device_errors).
+constexpr uint32_t kErrSlot = 4u;  // a slot or page outside the cache: skipped
+constexpr uint32_t kErrPlan = 8u;  // a plan ran out of free pages, table columns or token rows
+
+// The cache: [pages, kv_heads, page / 16] atoms of 16 tokens (18 * D bytes each,
+// keys and values of one kv head; the byte order is in nq.h).  Pages lie
+// page_stride bytes apart.
+struct KvCache {
+  uint8_t* base;
+  int64_t page_stride;
+  int64_t pages;
+  int32_t heads;
+  int32_t log_page;  // log2(tokens per page), 4 .. 7
+  int32_t d;
+};
+
+struct KvPlanArgs {
+  const int32_t* cached;   // [B] tokens each request holds already
+  const int32_t* added;    // [B] tokens it gains
+  int32_t* table;          // [B, ld_table] page numbers, `width` columns used
+  int64_t ld_table;
+  const int32_t* free_pages;  // [n_free]
+  const int32_t* free_head;   // [1] first entry of the list not yet taken
+  int32_t* free_head_out;     // [1]
+  int32_t* cu_q;       // [B + 1]
+  int32_t* kv_lens;    // [B]
+  int32_t* positions;  // [T]
+  int64_t* slots;      // [T]
+  int32_t B, T, width, n_free, log_page;
+  uint32_t* err;
+};
+
+struct KvCopyArgs {  // append (bf16 -> cache) and gather (cache -> bf16)
+  uint16_t* k;       // bf16 [T, heads, d] with token and head strides (elements)
+  uint16_t* v;
+  int64_t ld_kt, ld_kh, ld_vt, ld_vh;
+  const int64_t* slots;  // [T], < 0: a padding token
+  const float* k_scale;
+  const float* v_scale;
+  KvCache cache;
+  int32_t T;
+  uint32_t* err;
+};
+
+struct AttnArgs {
+  const uint16_t* q;  // bf16 [T, heads, d]
+  int64_t ld_qt, ld_qh;
+  KvCache cache;
+  const int32_t* table;
+  int64_t ld_table;
+  int32_t width;  // columns of the table
+  const int32_t* kv_lens;
+  const int32_t* cu_q;
+  const float* k_scale;
+  const float* v_scale;
+  uint16_t* out;  // bf16 [T, heads, d]
+  int64_t ld_ot, ld_oh;
+  float* lse;  // [T, ld_lse] or null
+  int64_t ld_lse;
+  uint32_t* counters;  // arrivals per split tile, zero between calls
+  float* partials;
+  int32_t T, B, heads, group;  // group: query heads per kv head
+  int32_t window;              // 0: none
+  int32_t causal;
+  float scale_log2;  // softmax scale * log2(e)
+  int32_t max_splits;
+  uint32_t* err;
+};
+
+// Counters at the head of the attention workspace; partial results follow.
+constexpr int kAttnCounters = 16384;
+
+// Kernels (nullptr: not built).
+const void* kv_plan_kernel();
+const void* kv_append_kernel(int d, bool vec);
+const void* kv_gather_kernel(int d, bool vec);
+constexpr int kKvPlanThreads = 512;
+constexpr int kKvCopyThreads = 256;
+
+constexpr int kAttnRowsThreads = 128;
+const void* attn_rows_kernel(int d, int n_tiles);       // n_tiles: 8-row tiles per warp, 1 or 2
+size_t attn_rows_smem(int d, int n_tiles);
+
+}  // namespace nq

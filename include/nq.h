@@ -7,7 +7,9 @@
  * quantizes the float32 result once, to e4m3 (FP8) or to NVFP4 (packed e2m1 +
  * e4m3 block scales).  A fifth call quantizes raw bf16 activations per group
  * of 128 (or 64) elements, and a sixth fuses RMSNorm with that group
- * quantization.
+ * quantization.  Four more keep a paged key/value cache in NVFP4: they lay a
+ * step's tokens out in pages, append them, read them back and attend over them
+ * ("The key/value cache", below).
  *
  * Conventions shared by every call
  * --------------------------------
@@ -153,6 +155,9 @@ typedef enum nq_status {
  * and 7 are not built (NQ_ERR_UNSUPPORTED).  0 = automatic. */
 #define NQ_FLAG_VARIANT(n) ((((uint32_t)(n)) & 0x7u) << 24)
 #define NQ_FLAG_VARIANT_MASK (0x7u << 24)
+/* Attention only: every key of the request is in sight of every query row (the
+ * default is causal). */
+#define NQ_FLAG_NONCAUSAL (1u << 9)
 /* Library version (major * 10000 + minor * 100 + patch). */
 int nq_version(void);
 /* Static text of a status code. */
@@ -161,7 +166,9 @@ const char* nq_status_string(nq_status status);
  * reads and clears this library's device error word in one atomic step.
  * NQ_OK if no kernel recorded an error since the last check; NQ_ERR_CUDA
  * (message in nq_last_error) if a MoE destination row was out of range (bit 1:
- * that store was skipped, the other rows are written), or if the device
+ * that store was skipped, the other rows are written), a slot or page lay
+ * outside the key/value cache (bit 2: skipped), a key/value plan ran out of
+ * pages, table columns or token rows (bit 3), or if the device
  * reported an error while synchronizing.  Kernels never trap or hang, and no
  * kernel of this library waits on anything. */
 nq_status nq_check_device_errors(void);
@@ -332,6 +339,130 @@ nq_status nq_rmsnorm_quant_nvfp4(const void* x, int64_t ld_x, const void* residu
                                  void* sf_out, int64_t ld_sf, void* norm_out, int64_t ld_norm,
                                  int64_t M, int64_t d, float eps, uint32_t flags,
                                  nq_stream_t stream);
+
+/*
+ * ---- The key/value cache ----
+ * A paged cache of attention keys and values in NVFP4 (e2m1 codes, one e4m3
+ * scale per 16 dimensions, a float32 global scale each for keys and values).
+ * A page holds page_size tokens (16, 32, 64 or 128) of every kv head; a slot is
+ * page * page_size + the token's place in its page; a request's pages are
+ * listed, in order, in its row of the block table.  Head dimension d: 64, 128
+ * or 256.
+ *
+ * Memory: uint8 [num_pages] pages, page_stride bytes apart (a multiple of 16, so
+ * that one allocation may hold the pages of several layers side by side), each
+ * [kv_heads, page_size / 16] atoms of 18 * d bytes: 16 consecutive tokens of one
+ * kv head.  An atom is, in this order,
+ *   key codes 8 d | value codes 8 d | key scales d | value scales d (bytes),
+ * with n = d / 64, w = max(1, d / 128), token t = 0..15 and block b = 0..d/16-1
+ * of 16 dimensions (8 bytes; dimension 2i in the low nibble of byte i):
+ *   key codes    s = (t/8) n + b%n, lane = 4 (t%8) + b/n:
+ *                (s/2) 512 + 16 lane + 8 (s%2)
+ *   key scales   2 n lane + s
+ *   value codes  i = 2 (t/8) + t%2, j = (t/2)%4; byte y = 0..d/2-1 of the token:
+ *                r = y / (d/16), x = i (d/16) + y%(d/16):
+ *                (x/16) 512 + 16 (4 r + j) + x%16
+ *   value scales 4 w (4 (b/w) + j) + i w + b%w
+ * (integer divisions): the order in which the lanes of a warp take keys and
+ * values into a 16 x 8 x 16 matrix product.  Every byte belongs to one token.
+ */
+
+/* Most requests a plan takes. */
+#define NQ_KV_MAX_REQUESTS 16384
+/* Bytes of the workspace nq_attention_nvfp4_kv needs, whatever the sizes. */
+#define NQ_ATTENTION_WORKSPACE_BYTES (32 << 20)
+
+/* Bytes of one page of all kv heads (the smallest page_stride):
+ * kv_heads * page_size * d * 9 / 8. */
+int64_t nq_kv_page_bytes(int32_t kv_heads, int32_t d, int32_t page_size);
+
+/*
+ * Block table rows, slots and positions of a step's tokens, from the requests'
+ * lengths, on the device.
+ *   cached_lens int32 [B]  tokens each request holds; new_lens int32 [B] tokens
+ *     it gains in this step (0 allowed).
+ *   block_table int32 [B, ld_table], table_width columns used: column i of row b
+ *     is the page of tokens i * page_size ...  The call fills the columns from
+ *     ceil(cached / page_size) to ceil((cached + new) / page_size) - 1, taking
+ *     pages in request order from free_pages int32 [n_free] at entry
+ *     free_head[0], and leaves every other column as it was.
+ *   free_head_out int32 [1]  free_head[0] + the pages taken.  May equal
+ *     free_head: a replayed graph then takes further pages each time.
+ *   cu_q int32 [B + 1]  first token row of each request and their total;
+ *   kv_lens int32 [B]   cached + new;
+ *   positions int32 [T], slots int64 [T]  of the tokens, request after request;
+ *     rows behind the last token (a padded batch) get -1.
+ * A request that outgrows its table row, tokens past T and pages past the free
+ * list's end (table entry -1, slot -1) set bit 3 of the device error word;
+ * lengths are then cut to the table's width and cu_q to T.  Negative lengths
+ * count as 0 and set the same bit.  Integers only: results are exact.
+ * B <= NQ_KV_MAX_REQUESTS; table_width * page_size <= 2^30.  flags:
+ * NQ_FLAG_PDL.
+ */
+nq_status nq_kv_plan(const int32_t* cached_lens, const int32_t* new_lens, int32_t* block_table, int64_t ld_table,
+                     int32_t table_width, const int32_t* free_pages, int64_t n_free, const int32_t* free_head,
+                     int32_t* free_head_out, int32_t* cu_q, int32_t* kv_lens, int32_t* positions, int64_t* slots,
+                     int64_t B, int64_t T, int32_t page_size, uint32_t flags, nq_stream_t stream);
+
+/*
+ * Quantizes keys and values of T tokens into their slots.
+ *   k, v  bf16 [T, kv_heads, d], token and head strides in elements (slices of a
+ *     fused projection's output may be passed as they are);
+ *   slots int64 [T], < 0: a padding token, skipped; a slot past the last page is
+ *     skipped and sets bit 2 of the device error word.  A slot may occur once.
+ *   k_scale, v_scale float32 device [1]: global scales g, positive and finite,
+ *     read at kernel execution.
+ * Each block of 16: sf = e4m3(RN(RN(absmax / 6) / g)), codes e2m1(RN(x *
+ * RN(1 / RN(sf * g)))), as nq_rmsnorm_quant_nvfp4's default.  A NaN element
+ * takes no part in absmax.  flags: NQ_FLAG_PDL.
+ */
+nq_status nq_kv_append_nvfp4(const void* k, int64_t ld_k_token, int64_t ld_k_head, const void* v, int64_t ld_v_token,
+                             int64_t ld_v_head, const int64_t* slots, const float* k_scale, const float* v_scale,
+                             void* cache, int64_t page_stride, int64_t num_pages, int64_t T, int32_t kv_heads, int32_t d,
+                             int32_t page_size, uint32_t flags, nq_stream_t stream);
+
+/*
+ * Reads tokens back: k_out, v_out bf16 [T, kv_heads, d] = RN_bf16(RN(e2m1 * sf *
+ * g)).  slots as above, in any order and as often as wanted; slots < 0 and slots
+ * past the last page (bit 2) read as zeros.  flags: NQ_FLAG_PDL.
+ */
+nq_status nq_kv_gather_nvfp4(const void* cache, int64_t page_stride, int64_t num_pages, const int64_t* slots,
+                             const float* k_scale, const float* v_scale, void* k_out, int64_t ld_k_token,
+                             int64_t ld_k_head, void* v_out, int64_t ld_v_token, int64_t ld_v_head, int64_t T,
+                             int32_t kv_heads, int32_t d, int32_t page_size, uint32_t flags, nq_stream_t stream);
+
+/*
+ * Attention of a ragged batch over the cache: prompts, chunks of prompts, single
+ * tokens and any mixture of them.
+ *   q bf16 [T, heads, d], out bf16 [T, heads, d], token and head strides in
+ *     elements; request b owns rows cu_q[b] ... cu_q[b + 1] - 1 and its row i has
+ *     position kv_lens[b] - (cu_q[b + 1] - cu_q[b]) + i.  Rows no request owns
+ *     are left as they were.  heads % kv_heads == 0; query head h reads kv head
+ *     h / (heads / kv_heads).
+ *   Keys in sight of position p: j < kv_lens[b], j <= p (unless
+ *     NQ_FLAG_NONCAUSAL), and with window > 0 j > p - window.
+ *   s_j = softmax_scale * k_scale[0] * <q, e2m1 * sf of key j>, p = softmax(s),
+ *   out = RN_bf16(v_scale[0] * sum_j p_j (e2m1 * sf of value j)); a row without
+ *     keys gives zeros.
+ *   lse float32 [T, ld_lse] (ld_lse >= heads) log sum_j exp(s_j), -inf for a row
+ *     without keys; or NULL.
+ *   workspace: NQ_ATTENTION_WORKSPACE_BYTES of device memory, 16-byte aligned,
+ *     zero-filled before its first use; every call leaves it ready for the next.
+ *     Calls that may run at the same time need one each.
+ * Sums, softmax statistics and accumulators are float32; softmax weights are
+ * rounded to f16 before they meet the values.  Results do not depend on timing.
+ * A page outside the cache is skipped, its keys count as out of sight, and bit 2
+ * of the device error word is set.  Memory behind a request's last key is never
+ * used, whatever it holds.  table_width * page_size <= 2^30; a longer kv_len is
+ * cut to it.  flags: NQ_FLAG_PDL, NQ_FLAG_NONCAUSAL.
+ */
+nq_status nq_attention_nvfp4_kv(const void* q, int64_t ld_q_token, int64_t ld_q_head, const void* cache,
+                                int64_t page_stride, int64_t num_pages, const int32_t* block_table, int64_t ld_table,
+                                int32_t table_width, const int32_t* kv_lens, const int32_t* cu_q, const float* k_scale,
+                                const float* v_scale, void* out, int64_t ld_out_token, int64_t ld_out_head, float* lse,
+                                int64_t ld_lse, void* workspace, int64_t workspace_bytes, int64_t T, int64_t B,
+                                int32_t heads, int32_t kv_heads, int32_t d, int32_t page_size, float softmax_scale,
+                                int32_t window, uint32_t flags, nq_stream_t stream);
 
 #ifdef __cplusplus
 } /* extern "C" */
