@@ -608,7 +608,8 @@ nq_status nq_check_device_errors(void) {
   if (word == 0) return NQ_OK;
   return fail(NQ_ERR_CUDA, "%s: device error word 0x%x (bit 1: a MoE destination row was out of range; its "
               "store was skipped; bit 2: a slot or page outside the key/value cache; bit 3: a key/value plan ran out "
-              "of pages, table columns or token rows)", fn, word);
+              "of pages, table columns or token rows; bit 4: a bounded wait of an attention kernel ran out, its output is not "
+              "valid)", fn, word);
 }
 
 nq_status nq_query_schedule(int op, int64_t M, int64_t d, uint32_t flags, int* threads_per_row,

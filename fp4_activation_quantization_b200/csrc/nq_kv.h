@@ -12,6 +12,7 @@ namespace nq {
 // Bits of the device error word that these kernels set (read and cleared by
 // nq_check_device_errors).
 constexpr uint32_t kErrSlot = 4u;  // a slot or page outside the cache: skipped
+constexpr uint32_t kErrWait = 16u;  // a bounded wait inside a kernel ran out: its output is not valid
 constexpr uint32_t kErrPlan = 8u;  // a plan ran out of free pages, table columns or token rows
 
 // The cache: [pages, kv_heads, page / 16] atoms of 16 tokens (18 * D bytes each,
@@ -75,7 +76,9 @@ struct AttnArgs {
   int32_t window;              // 0: none
   int32_t causal;
   float scale_log2;  // softmax scale * log2(e)
-  int32_t max_splits;
+  int32_t max_splits;  // rows kernel: parts of a segment on average, at most
+  int32_t tiles;       // tiles kernel: row tiles counted over the batch
+  int32_t splits;      // tiles kernel: parts of an item's keys
   uint32_t* err;
 };
 
@@ -92,5 +95,14 @@ constexpr int kKvCopyThreads = 256;
 constexpr int kAttnRowsThreads = 128;
 const void* attn_rows_kernel(int d, int n_tiles);       // n_tiles: 8-row tiles per warp, 1 or 2
 size_t attn_rows_smem(int d, int n_tiles);
+
+constexpr int kAttnTilesThreads = 512;
+struct AttnTiles {
+  const void* kernel;
+  const void* join;  // 256 threads, 8 rows a CTA; only after a kernel with splits > 1
+  int rows;          // of a CTA
+  size_t smem;
+};
+AttnTiles attn_tiles(int d);
 
 }  // namespace nq

@@ -226,6 +226,31 @@ nq_status nq_attention_nvfp4_kv(const void* q, int64_t ld_q_token, int64_t ld_q_
   if (a.err == nullptr) return error(NQ_ERR_CUDA, "%s: no CUDA device", fn);
 
   const int64_t rows = (T * a.group + B - 1) / B;  // of an average request and kv head
+  if (rows > 16) {
+    const nq::AttnTiles k = nq::attn_tiles(d);
+    if (!nq::host::allow_smem(k.kernel, k.smem))
+      return error(NQ_ERR_UNSUPPORTED, "%s: %zu bytes of shared memory not available", fn, k.smem);
+    const int64_t tiles = T * a.group / k.rows + B, items = tiles * kv_heads;
+    const int64_t sms = nq::host::resident_ctas(k.kernel, nq::kAttnTilesThreads, k.smem);
+    if (sms <= 0) return error(NQ_ERR_CUDA, "%s: no CUDA device", fn);
+    const int64_t room = (workspace_bytes - int64_t(sizeof(uint32_t)) * nq::kAttnCounters) /
+                         (int64_t(k.rows) * (d + 2) * int64_t(sizeof(float)));
+    int64_t splits = (sms < room ? sms : room) / items;
+    const int64_t blocks = (int64_t(table_width) * page_size + 511) / 512;  // at least four blocks of keys each
+    splits = splits < blocks ? splits : blocks;
+    splits = splits < 1 ? 1 : splits;
+    const int64_t grid = items * splits, join_grid = items * (k.rows / 8);
+    if (grid > kInt32Max || join_grid > kInt32Max) return error(NQ_ERR_UNSUPPORTED, "%s: T or B too large", fn);
+    a.tiles = int32_t(tiles);
+    a.splits = int32_t(splits);
+    void* args[] = {&a};
+    nq_status s = nq::host::launch(fn, k.kernel, unsigned(grid), nq::kAttnTilesThreads, k.smem, args,
+                                   (flags & NQ_FLAG_PDL) != 0, static_cast<cudaStream_t>(stream));
+    if (s == NQ_OK && splits > 1)
+      s = nq::host::launch(fn, k.join, unsigned(join_grid), 256, 0, args, (flags & NQ_FLAG_PDL) != 0,
+                           static_cast<cudaStream_t>(stream));
+    return s;
+  }
   const int n_tiles = rows <= 8 ? 1 : 2;
   const void* k = nq::attn_rows_kernel(d, n_tiles);
   const size_t smem = nq::attn_rows_smem(d, n_tiles);

@@ -284,6 +284,20 @@ def test_prompts(nq, heads, kv_heads, D, window, causal):
     check(nq, s, window=window, causal=causal)
 
 
+@pytest.mark.parametrize("heads,kv_heads,D", [(16, 4, 64), (16, 4, 128), (16, 4, 256)])
+def test_many_chunks_from_a_cold_cache(nq, heads, kv_heads, D):
+    """More tiles than the GPU holds at once, first with the cache's bytes out of L2 (slow), then in it: the same bits."""
+    s = make(nq, [400] * 12, [700 + 60 * i for i in range(12)], heads, kv_heads, D, 64, seed=15)
+    flush = torch.empty(256 << 20, dtype=torch.uint8, device="cuda")
+    outs = []
+    for i in range(4):
+        if i % 2 == 0:
+            flush.fill_(i)
+        outs.append(check(nq, s))
+    for out, lse in outs[1:]:
+        assert torch.equal(out, outs[0][0]) and torch.equal(lse, outs[0][1])
+
+
 @pytest.mark.parametrize("D", [64, 128, 256])
 def test_prompt_rows_beyond_the_keys(nq, D):
     check(nq, make(nq, [300, 200], [130, 0], 8, 2, D, 16, seed=4))
