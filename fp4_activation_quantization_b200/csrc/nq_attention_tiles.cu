@@ -90,6 +90,11 @@ __device__ __forceinline__ void fence_smem_to_mma() { asm volatile("fence.proxy.
 __device__ __forceinline__ void commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+  return one != 0;
+}
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
   asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
                ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(uint32_t(accumulate))
@@ -426,7 +431,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
       lo = (a.window > 0 ? int(max(int64_t(0), pos + 1 - a.window)) : 0) - it.first;
     }
     float m = -INFINITY;
-    float2 l2 = make_float2(0.0f, 0.0f);
+    float2 l2[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
     const uint32_t o_addr = tmem + lanes + C::kOCol + t * D;
     bool ok = t < tiles;
     for (int i = 0; ok && i < n; ++i) {
@@ -446,16 +451,21 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
         for (int e = 0; e < 128; ++e)
           if (k0 + e < lo || k0 + e >= hi || ((bad >> (e / 16)) & 1u)) sv[e] = 0xFF800000u;  // -inf
       }
-      float top = __uint_as_float(sv[0]);
+      float tops[4];
 #pragma unroll
-      for (int e = 1; e < 127; e += 2) top = fmax3(top, __uint_as_float(sv[e]), __uint_as_float(sv[e + 1]));
-      top = fmaxf(top, __uint_as_float(sv[127])) * c;
+      for (int y = 0; y < 4; ++y) {
+        tops[y] = fmaxf(__uint_as_float(sv[32 * y]), __uint_as_float(sv[32 * y + 1]));
+#pragma unroll
+        for (int e = 2; e < 32; e += 2)
+          tops[y] = fmax3(tops[y], __uint_as_float(sv[32 * y + e]), __uint_as_float(sv[32 * y + e + 1]));
+      }
+      const float top = fmaxf(fmax3(tops[0], tops[1], tops[2]), tops[3]) * c;
       const bool raise = top > m + kRaise;
       if (__any_sync(kFull, raise)) {
         const float f = raise ? ex2(m - top) : 1.0f;
         if (raise) m = top;
-        l2.x *= f;
-        l2.y *= f;
+#pragma unroll
+        for (int y = 0; y < 2; ++y) l2[y] = make_float2(l2[y].x * f, l2[y].y * f);
         if (i > 0) {
           // Tiles in turn: S of block i was issued after P V of block i - 1, so O
           // is at rest.  Two S buffers: S of block i was issued after P V of block
@@ -488,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
           const float2 v = __ffma2_rn(make_float2(__uint_as_float(sv[64 * p + 2 * e]), __uint_as_float(sv[64 * p + 2 * e + 1])),
                                       c2, nm2);
           const float2 w = make_float2(ex2(v.x), ex2(v.y));
-          l2 = __fadd2_rn(l2, w);
+          l2[e & 1] = __fadd2_rn(l2[e & 1], w);
           pv[e] = pack_f16x2(w.x, w.y);
         }
         tmem_store32(s_addr + 32 * p, pv);
@@ -503,7 +513,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
       ok = mbar_wait_warp(o_last, 0, gave_up);
       fence_after();
     }
-    const float l = l2.x + l2.y;
+    const float l = (l2[0].x + l2[0].y) + (l2[1].x + l2[1].y);
     const int64_t at = it.q0 + token;
     float* part = nullptr;
     if (a.splits > 1) part = a.partials + (int64_t(it.index) * a.splits + it.split) * (C::kRows * (D + 2)) + row * D;
@@ -645,85 +655,111 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
   } else {
     // ----------------------------------------------------------- products ----
     regs_dec<C::kRegsMma>();
-    if (warp == 12 && lane == 0 && n > 0) {
+    if (warp == 12 && n > 0) {
+      // The whole warp walks the loop, so that descriptors and counters stay in
+      // uniform registers; one elected lane issues.  Rolled loops: this code runs
+      // for a moment between long waits, and unrolled it was slowed to 100 cycles
+      // per product by instruction fetches (a prompt of 8192: 757 us).
+      const bool leader = elect_one();
+      const uint32_t tm = __shfl_sync(kFull, tmem, 0);
       constexpr uint32_t kIdQK = instruction(kBlock, false), kIdPV = instruction(D, true);
-      bool ok = mbar_wait(q_full, 0, gave_up);
+      bool ok = mbar_wait_warp(q_full, 0, gave_up);
       fence_after();
       auto wait_slot = [&](int q) {
-        ok = ok && mbar_wait(full(q % C::kSlots), (q / C::kSlots) & 1, gave_up);
+        ok = ok && mbar_wait_warp(full(q % C::kSlots), (q / C::kSlots) & 1, gave_up);
         fence_after();
       };
+      auto arrive = [&](uint32_t bar) {
+        if (leader) commit(bar);
+        __syncwarp();
+      };
       auto qk = [&](int t, int s_col, int q) {
-        const uint64_t qd = matrix(qs + t * C::kQBytes), kd = matrix(ring + (q % C::kSlots) * C::kSlotBytes);
+        uint64_t qd = matrix(qs + t * C::kQBytes), kd = matrix(ring + (q % C::kSlots) * C::kSlotBytes);
+#pragma unroll 1
+        for (int k = 0; k < C::kChunks; ++k) {
+          if (leader) {
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint64_t step = uint64_t((k / 4) * 16384 + (k % 4) * 32) >> 4;
-          mma_ss(tmem + s_col, qd + step, kd + step, kIdQK, k > 0);
+            for (int x = 0; x < 4; ++x) mma_ss(tm + s_col, qd + 2 * x, kd + 2 * x, kIdQK, k > 0 || x > 0);
+          }
+          __syncwarp();
+          qd += 16384 >> 4;
+          kd += 16384 >> 4;
         }
       };
       auto pv = [&](int t, int s_col, int q, bool first) {
-        const uint64_t vd = matrix(ring + (q % C::kSlots) * C::kSlotBytes);
+        uint64_t vd = matrix(ring + (q % C::kSlots) * C::kSlotBytes);
+        const uint32_t o = tm + C::kOCol + t * D;
+        uint32_t p = tm + s_col;
+#pragma unroll 1
+        for (int k = 0; k < kBlock / 64; ++k) {
+          if (leader) {
 #pragma unroll
-        for (int k = 0; k < kBlock / 16; ++k)
-          mma_ts(tmem + C::kOCol + t * D, tmem + s_col + 8 * k, vd + (uint64_t(k * 2048) >> 4), kIdPV, k > 0 || !first);
+            for (int x = 0; x < 4; ++x) mma_ts(o, p + 8 * x, vd + x * (2048 >> 4), kIdPV, k > 0 || x > 0 || !first);
+          }
+          __syncwarp();
+          p += 32;
+          vd += 8192 >> 4;
+        }
       };
       if constexpr (C::kTiles == 2) {
         wait_slot(0);
         for (int t = 0; t < tiles && ok; ++t) {
           qk(t, 128 * t, 0);
-          commit(s_full(t));
+          arrive(s_full(t));
         }
-        if (ok) commit(empty(0));
+        if (ok) arrive(empty(0));
+#pragma unroll 1
         for (int i = 0; i < n && ok; ++i) {
           const int qv = 2 * i + 1, qn = 2 * i + 2;
           wait_slot(qv);
           if (i + 1 < n) wait_slot(qn);
+#pragma unroll 1
           for (int t = 0; t < tiles && ok; ++t) {
-            if (!(ok = mbar_wait(p_full(t), i & 1, gave_up))) break;
+            if (!(ok = mbar_wait_warp(p_full(t), i & 1, gave_up))) break;
             fence_after();
             pv(t, 128 * t, qv, i == 0);
             if (i + 1 < n) {
               qk(t, 128 * t, qn);
-              commit(s_full(t));
+              arrive(s_full(t));
             }
           }
           if (!ok) break;
-          commit(empty(qv % C::kSlots));
-          if (i + 1 < n) commit(empty(qn % C::kSlots));
+          arrive(empty(qv % C::kSlots));
+          if (i + 1 < n) arrive(empty(qn % C::kSlots));
         }
-        if (ok) commit(o_last);
+        if (ok) arrive(o_last);
       } else {
         // K0 K1 V0 K2 V1 ... K(n-1) V(n-2) V(n-1)
         wait_slot(0);
         if (ok) {
           qk(0, 0, 0);
-          commit(s_full(0));
-          commit(empty(0));
+          arrive(s_full(0));
+          arrive(empty(0));
         }
         int q = 1;
+#pragma unroll 1
         for (int i = 0; i < n && ok; ++i) {
           if (i + 1 < n) {
             wait_slot(q);
             if (!ok) break;
             qk(0, 128 * ((i + 1) & 1), q);
-            commit(s_full((i + 1) & 1));
-            commit(empty(q % C::kSlots));
+            arrive(s_full((i + 1) & 1));
+            arrive(empty(q % C::kSlots));
             ++q;
           }
           wait_slot(q);
-          if (!ok || !(ok = mbar_wait(p_full(i & 1), (i >> 1) & 1, gave_up))) break;
+          if (!ok || !(ok = mbar_wait_warp(p_full(i & 1), (i >> 1) & 1, gave_up))) break;
           fence_after();
           pv(0, 128 * (i & 1), q, i == 0);
-          commit(empty(q % C::kSlots));
-          commit(o_done);
+          arrive(empty(q % C::kSlots));
+          arrive(o_done);
           ++q;
         }
-        if (ok) commit(o_last);
+        if (ok) arrive(o_last);
       }
       if (!ok) {
         // Products in flight end before their tensor memory is freed.
-        atomicOr(a.err, kErrWait);
-        commit(drained);
+        arrive(drained);
         for (int i = 0; i < (1 << 20) && !mbar_try(drained, 0); ++i) {
         }
       }
