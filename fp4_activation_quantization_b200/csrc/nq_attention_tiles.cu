@@ -327,7 +327,7 @@ template <int D>
 __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
   using C = Cfg<D>;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t s_bar[24];
+  __shared__ __align__(8) uint64_t s_bar[28];
   __shared__ uint32_t s_tmem, s_bad[kBad];
   __shared__ int s_found, s_gave_up;
 
@@ -336,25 +336,31 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
   const uint32_t ring = smem, qs = smem + 131072;
   const uint32_t bars = smem_u32(s_bar);
   auto full = [&](int s) { return bars + 8 * s; };          // a slot holds its block
-  auto empty = [&](int s) { return bars + 64 + 8 * s; };    // a slot's products are done
+  auto empty = [&](int s) { return bars + 64 + 8 * s; };    // products that read a slot are done
   auto s_full = [&](int t) { return bars + 128 + 8 * t; };  // S of a tile (or buffer)
-  auto p_full = [&](int t) { return bars + 144 + 8 * t; };  // P of a tile (or buffer)
-  const uint32_t q_full = bars + 160, o_done = bars + 168, o_last = bars + 176, drained = bars + 184;
+  auto p_full = [&](int t, int half) { return bars + 144 + 16 * t + 8 * half; };  // 64 keys of P of a tile (or buffer)
+  const uint32_t q_full = bars + 176, o_done = bars + 184;
+  auto o_last = [&](int t) { return bars + 192 + 8 * t; };   // the last P V of a tile
+  auto drained = [&](int t) { return bars + 208 + 8 * t; };  // after a wait ran out
 
   if (tid == 0) {
-    for (int s = 0; s < C::kSlots; ++s) {
+    for (int s = 0; s < 8; ++s) {
       mbar_init(full(s), C::kProducerWarps);
       mbar_init(empty(s), 1);
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(s_full(t), 1);
-      mbar_init(p_full(t), 4);
+      mbar_init(p_full(t, 0), 4);
+      mbar_init(p_full(t, 1), 4);
     }
     mbar_init(q_full, 4 * C::kTiles);
     mbar_init(o_done, 1);
-    mbar_init(o_last, 1);
-    mbar_init(drained, 1);
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(o_last(t), 1);
+      mbar_init(drained(t), 1);
+    }
     s_gave_up = 0;
+    for (int i = 0; i < kBad; ++i) s_bad[i] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   griddep_wait();
@@ -430,6 +436,13 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
       hi = (a.causal ? int(min(int64_t(it.kv_len), max(int64_t(0), pos + 1))) : it.kv_len) - it.first;
       lo = (a.window > 0 ? int(max(int64_t(0), pos + 1 - a.window)) : 0) - it.first;
     }
+    // Blocks that every row of the warp sees whole need no mask.
+    int lo_all = live ? lo : -0x7fffffff, hi_all = live ? hi : 0x7fffffff;
+#pragma unroll
+    for (int w = 1; w < 32; w <<= 1) {
+      lo_all = max(lo_all, __shfl_xor_sync(kFull, lo_all, w));
+      hi_all = min(hi_all, __shfl_xor_sync(kFull, hi_all, w));
+    }
     float m = -INFINITY;
     float2 l2[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
     const uint32_t o_addr = tmem + lanes + C::kOCol + t * D;
@@ -446,7 +459,8 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
       tmem_wait_load();
       const uint32_t bad = s_bad[i % kBad];
       const int k0 = i * kBlock;
-      if (__any_sync(kFull, lo > k0 || hi < k0 + kBlock) || bad) {
+      const bool masked = k0 < lo_all || k0 + kBlock > hi_all || bad != 0;
+      if (masked) {
 #pragma unroll
         for (int e = 0; e < 128; ++e)
           if (k0 + e < lo || k0 + e >= hi || ((bad >> (e / 16)) & 1u)) sv[e] = 0xFF800000u;  // -inf
@@ -490,27 +504,29 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
       const float2 c2 = make_float2(c, c);
       const float nm = m == -INFINITY ? 0.0f : -m;
       const float2 nm2 = make_float2(nm, nm);
+      // Two halves of 64 keys, each handed over on its own, so that P V starts
+      // under the second half's exponentials.
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
         uint32_t pv[32];
 #pragma unroll
         for (int e = 0; e < 32; ++e) {
-          const float2 v = __ffma2_rn(make_float2(__uint_as_float(sv[64 * p + 2 * e]), __uint_as_float(sv[64 * p + 2 * e + 1])),
-                                      c2, nm2);
+          const float2 v = __ffma2_rn(
+              make_float2(__uint_as_float(sv[64 * p + 2 * e]), __uint_as_float(sv[64 * p + 2 * e + 1])), c2, nm2);
           const float2 w = make_float2(ex2(v.x), ex2(v.y));
           l2[e & 1] = __fadd2_rn(l2[e & 1], w);
           pv[e] = pack_f16x2(w.x, w.y);
         }
         tmem_store32(s_addr + 32 * p, pv);
+        tmem_wait_store();
+        fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full(buf, p));
       }
-      tmem_wait_store();
-      fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(p_full(buf));
     }
     // ---- output: this thread's row
     if (ok && n > 0) {
-      ok = mbar_wait_warp(o_last, 0, gave_up);
+      ok = mbar_wait_warp(o_last(t), 0, gave_up);
       fence_after();
     }
     const float l = (l2[0].x + l2[0].y) + (l2[1].x + l2[1].y);
@@ -599,7 +615,14 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
     auto convert = [&](const Raw& raw, int block, bool value) {
       const int slot = q % C::kSlots, round = q / C::kSlots;
       ++q;
-      if (round > 0 && !(ok = mbar_wait_warp(empty(slot), (round - 1) & 1, gave_up))) return;
+      if (C::kTiles == 2) {
+        // Releases: 0 of K(0), then 1 + i of V(i) and K(i + 1) together, counted
+        // over eight barriers.
+        const int release = (value ? block + 1 : block) - C::kSlots / 2;
+        if (round > 0 && !(ok = mbar_wait_warp(empty(release % 8), (release / 8) & 1, gave_up))) return;
+      } else {
+        if (round > 0 && !(ok = mbar_wait_warp(empty(slot), (round - 1) & 1, gave_up))) return;
+      }
 #pragma unroll
       for (int i = 0; i < kMine; ++i)
         convert_atom<D>(raw.atom[i], ring + slot * C::kSlotBytes, 16 * (pw + C::kProducerWarps * i), value,
@@ -656,7 +679,8 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
     // ----------------------------------------------------------- products ----
     regs_dec<C::kRegsMma>();
     if (warp == 12 && n > 0) {
-      // The whole warp walks the loop, so that descriptors and counters stay in
+      // A warp for each tile (on schedulers of their own), so that neither tile's
+      // hand-overs wait behind the other's.  The whole warp walks the loop, so that descriptors and counters stay in
       // uniform registers; one elected lane issues.  Rolled loops: this code runs
       // for a moment between long waits, and unrolled it was slowed to 100 cycles
       // per product by instruction fetches (a prompt of 8192: 757 us).
@@ -686,12 +710,14 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
           kd += 16384 >> 4;
         }
       };
-      auto pv = [&](int t, int s_col, int q, bool first) {
+      auto pv = [&](int t, int buf, uint32_t parity, int q, bool first) {
         uint64_t vd = matrix(ring + (q % C::kSlots) * C::kSlotBytes);
         const uint32_t o = tm + C::kOCol + t * D;
-        uint32_t p = tm + s_col;
+        uint32_t p = tm + 128 * buf;
 #pragma unroll 1
-        for (int k = 0; k < kBlock / 64; ++k) {
+        for (int k = 0; k < 2; ++k) {
+          if (!(ok = mbar_wait_warp(p_full(buf, k), parity, gave_up))) return;
+          fence_after();
           if (leader) {
 #pragma unroll
             for (int x = 0; x < 4; ++x) mma_ts(o, p + 8 * x, vd + x * (2048 >> 4), kIdPV, k > 0 || x > 0 || !first);
@@ -710,24 +736,20 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
         if (ok) arrive(empty(0));
 #pragma unroll 1
         for (int i = 0; i < n && ok; ++i) {
+          // The producers fill V(i) before K(i + 1): one wait covers both.
           const int qv = 2 * i + 1, qn = 2 * i + 2;
-          wait_slot(qv);
-          if (i + 1 < n) wait_slot(qn);
+          wait_slot(i + 1 < n ? qn : qv);
 #pragma unroll 1
           for (int t = 0; t < tiles && ok; ++t) {
-            if (!(ok = mbar_wait_warp(p_full(t), i & 1, gave_up))) break;
-            fence_after();
-            pv(t, 128 * t, qv, i == 0);
-            if (i + 1 < n) {
+            pv(t, t, i & 1, qv, i == 0);
+            if (ok && i + 1 < n) {
               qk(t, 128 * t, qn);
               arrive(s_full(t));
             }
           }
-          if (!ok) break;
-          arrive(empty(qv % C::kSlots));
-          if (i + 1 < n) arrive(empty(qn % C::kSlots));
+          if (ok) arrive(empty((i + 1) % 8));  // V(i) and K(i + 1)
         }
-        if (ok) arrive(o_last);
+        for (int t = 0; t < tiles && ok; ++t) arrive(o_last(t));
       } else {
         // K0 K1 V0 K2 V1 ... K(n-1) V(n-2) V(n-1)
         wait_slot(0);
@@ -748,19 +770,19 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
             ++q;
           }
           wait_slot(q);
-          if (!ok || !(ok = mbar_wait_warp(p_full(i & 1), (i >> 1) & 1, gave_up))) break;
-          fence_after();
-          pv(0, 128 * (i & 1), q, i == 0);
+          if (!ok) break;
+          pv(0, i & 1, (i >> 1) & 1, q, i == 0);
+          if (!ok) break;
           arrive(empty(q % C::kSlots));
           arrive(o_done);
           ++q;
         }
-        if (ok) arrive(o_last);
+        if (ok) arrive(o_last(0));
       }
       if (!ok) {
         // Products in flight end before their tensor memory is freed.
-        arrive(drained);
-        for (int i = 0; i < (1 << 20) && !mbar_try(drained, 0); ++i) {
+        arrive(drained(warp - 12));
+        for (int i = 0; i < (1 << 20) && !mbar_try(drained(warp - 12), 0); ++i) {
         }
       }
     }
