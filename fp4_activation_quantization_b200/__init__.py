@@ -506,55 +506,81 @@ def kv_cache_shape(num_pages: int, kv_heads: int, head_dim: int, page_size: int)
     return num_pages, kv_heads, page_size * head_dim * 9 // 8
 
 
-def _launch(device, name, *args, stream=None) -> None:
-    """Call ``name`` on ``device``, the stream last; the device context is entered only when it is another one."""
-    index = device.index
-    if index is None or index == torch.cuda.current_device():
-        status = getattr(_get_lib(), name)(*args, _stream(stream))
+# These calls run once per layer and decode step, where a few microseconds of
+# argument checks would be the cost of the call: each tensor is asked for its
+# device, type, shape and strides once, and the current stream is read without
+# building a Stream object.
+def _launch(index: int, name: str, args, stream) -> None:
+    """Call ``name`` on device ``index``, the stream last; the device is switched to only when it is another one."""
+    if torch._C._cuda_getDevice() == index:
+        if stream is None:
+            stream = torch._C._cuda_getCurrentRawStream(index)
+        status = getattr(_get_lib(), name)(*args, stream if type(stream) is int else _stream(stream))
     else:
-        with torch.cuda.device(device):
+        with torch.cuda.device(index):
             status = getattr(_get_lib(), name)(*args, _stream(stream))
     if status != NQ_OK:
         raise NQError(status, name)
 
 
-def _ints(t, name: str, dtype, n: int):
-    _need(isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == dtype and t.shape == (n,)
-          and (n <= 1 or t.stride(0) == 1), f"{name} must be a contiguous {dtype} CUDA tensor [{n}]")
+def _device(t, name: str) -> int:
+    """Index of the CUDA device that tensor t lives on."""
+    _need(isinstance(t, torch.Tensor) and t.is_cuda, f"{name} must be a CUDA tensor")
+    return t.get_device()
 
 
-def _heads(t, name: str, d: int | None = None, heads: int | None = None):
-    """bf16 [T, heads, d] on CUDA, last dimension contiguous: (T, heads, d, token stride, head stride)."""
-    _need(isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == torch.bfloat16 and t.dim() == 3,
-          f"{name} must be a bfloat16 CUDA tensor [T, heads, d]")
-    T, H, D = t.shape
+def _vector(t, name: str, dtype, n, dev: int):
+    """Contiguous 1-D tensor of n elements (None: any number) on device dev; returns (length, address)."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.dim() == 1 and t.get_device() == dev
+            and t.is_contiguous() and (n is None or t.shape[0] == n)):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor [{'n' if n is None else n}] on cuda:{dev}")
+    return t.shape[0], t.data_ptr()
+
+
+def _one(t, name: str, dev: int) -> int:
+    if not (isinstance(t, torch.Tensor) and t.dtype is torch.float32 and t.numel() == 1 and t.get_device() == dev):
+        raise ValueError(f"{name} must be a one-element float32 tensor on cuda:{dev}")
+    return t.data_ptr()
+
+
+def _heads(t, name: str, dev: int, T=None, heads=None, d=None):
+    """bf16 [T, heads, d] on device dev, last dimension contiguous: (T, heads, d, token stride, head stride, address)."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16 and t.dim() == 3 and t.get_device() == dev):
+        raise ValueError(f"{name} must be a bfloat16 tensor [T, heads, d] on cuda:{dev}")
+    n, H, D = t.shape
     s0, s1, s2 = t.stride()
-    _need(s2 == 1, f"{name} must have a contiguous last dimension")
-    _need((d is None or D == d) and (heads is None or H == heads), f"{name} must be [T, {heads}, {d}], got {(T, H, D)}")
+    if (s2 != 1 and D > 1) or (T is not None and n != T) or (heads is not None and H != heads) or (d is not None and D != d):
+        raise ValueError(f"{name} must be [{T}, {heads}, {d}] with a contiguous last dimension, got {tuple(t.shape)} with "
+                         f"strides {t.stride()}")
     if H <= 1:
         s1 = max(s1, D)
-    if T <= 1:
-        s0 = max(s0, H * D if s1 <= D else (H - 1) * s1 + D)
-    return T, H, D, s0, s1
+    if n <= 1:
+        s0 = max(s0, H * D, (H - 1) * s1 + D)
+    return n, H, D, s0, s1, t.data_ptr()
 
 
-def _cache(cache, d: int):
-    """(pages, kv heads, tokens a page, page stride) of a cache tensor for head dimension d."""
-    _need(isinstance(cache, torch.Tensor) and cache.is_cuda and cache.dtype == torch.uint8 and cache.dim() == 3,
-          "cache must be a uint8 CUDA tensor of kv_cache_shape")
+def _cache(cache, d: int, dev: int):
+    """(pages, kv heads, tokens a page, page stride, address) of a cache tensor for head dimension d."""
+    if not (isinstance(cache, torch.Tensor) and cache.dtype is torch.uint8 and cache.dim() == 3 and cache.get_device() == dev):
+        raise ValueError(f"cache must be a uint8 tensor of kv_cache_shape on cuda:{dev}")
     pages, heads, n = cache.shape
     s0, s1, s2 = cache.stride()
-    _need(s2 == 1 and (heads <= 1 or s1 == n), "cache must be contiguous within a page")
-    _need(d > 0 and n * 8 % (9 * d) == 0, f"cache rows of {n} bytes hold no whole tokens of head dimension {d}")
-    return pages, heads, n * 8 // (9 * d), (s0 if pages > 1 else max(s0, heads * n))
+    if s2 != 1 or (heads > 1 and s1 != n):
+        raise ValueError("cache must be contiguous within a page")
+    if d < 1 or n * 8 % (9 * d):
+        raise ValueError(f"cache rows of {n} bytes hold no whole tokens of head dimension {d}")
+    return pages, heads, n * 8 // (9 * d), (s0 if pages > 1 else max(s0, heads * n)), cache.data_ptr()
 
 
-def _table(block_table, B: int):
-    _need(isinstance(block_table, torch.Tensor) and block_table.is_cuda and block_table.dtype == torch.int32
-          and block_table.dim() == 2 and block_table.shape[0] == B, f"block_table must be an int32 CUDA tensor [{B}, pages]")
-    width = block_table.shape[1]
-    _need(width <= 1 or block_table.stride(1) == 1, "block_table must have a contiguous last dimension")
-    return width, (block_table.stride(0) if B > 1 else max(block_table.stride(0), width))
+def _table(t, B: int, dev: int):
+    """(columns, row stride, address) of a block table of B rows."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is torch.int32 and t.dim() == 2 and t.get_device() == dev
+            and t.shape[0] == B):
+        raise ValueError(f"block_table must be an int32 tensor [{B}, pages] on cuda:{dev}")
+    width = t.shape[1]
+    s0, s1 = t.stride()
+    _need(width <= 1 or s1 == 1, "block_table must have a contiguous last dimension")
+    return width, (s0 if B > 1 else max(s0, width)), t.data_ptr()
 
 
 def nq_kv_plan(cached_lens, new_lens, block_table, free_pages, free_head, tokens: int, page_size: int, *,
@@ -568,26 +594,24 @@ def nq_kv_plan(cached_lens, new_lens, block_table, free_pages, free_head, tokens
     [B], positions int32 [tokens], slots int64 [tokens], free_head_out int32
     [1])``; pass ``free_head_out=free_head`` to advance the list in place.
     """
-    _need(isinstance(new_lens, torch.Tensor) and new_lens.dim() == 1, "new_lens must be an int32 CUDA tensor [B]")
-    B, dev = new_lens.shape[0], new_lens.device
-    _ints(cached_lens, "cached_lens", torch.int32, B)
-    _ints(new_lens, "new_lens", torch.int32, B)
-    width, ld = _table(block_table, B)
-    _need(isinstance(free_pages, torch.Tensor) and free_pages.dim() == 1, "free_pages must be an int32 CUDA tensor")
-    _ints(free_pages, "free_pages", torch.int32, free_pages.shape[0])
-    _ints(free_head, "free_head", torch.int32, 1)
+    dev = _device(new_lens, "new_lens")
+    B, new_p = _vector(new_lens, "new_lens", torch.int32, None, dev)
+    _, cached_p = _vector(cached_lens, "cached_lens", torch.int32, B, dev)
+    width, ld, table_p = _table(block_table, B, dev)
+    n_free, free_p = _vector(free_pages, "free_pages", torch.int32, None, dev)
+    _, head_p = _vector(free_head, "free_head", torch.int32, 1, dev)
     _need(tokens >= 0, "tokens must not be negative")
+    # One allocation for the int32 results.
+    cu_q, kv_lens, head_out, positions = torch.empty(2 * B + 2 + tokens, dtype=torch.int32, device=new_lens.device).split(
+        (B + 1, B, 1, tokens))
+    slots = torch.empty(tokens, dtype=torch.int64, device=new_lens.device)
     if free_head_out is None:
-        free_head_out = torch.empty(1, dtype=torch.int32, device=dev)
-    _ints(free_head_out, "free_head_out", torch.int32, 1)
-    _same_device(cached_lens, new_lens, block_table, free_pages, free_head, free_head_out)
-    cu_q = torch.empty(B + 1, dtype=torch.int32, device=dev)
-    kv_lens = torch.empty(B, dtype=torch.int32, device=dev)
-    positions = torch.empty(tokens, dtype=torch.int32, device=dev)
-    slots = torch.empty(tokens, dtype=torch.int64, device=dev)
-    _launch(dev, "nq_kv_plan", cached_lens.data_ptr(), new_lens.data_ptr(), block_table.data_ptr(), ld, width,
-            free_pages.data_ptr(), free_pages.shape[0], free_head.data_ptr(), free_head_out.data_ptr(), cu_q.data_ptr(),
-            kv_lens.data_ptr(), positions.data_ptr(), slots.data_ptr(), B, tokens, page_size, flags, stream=stream)
+        free_head_out = head_out
+    _, out_p = _vector(free_head_out, "free_head_out", torch.int32, 1, dev)
+    cu_p = cu_q.data_ptr()
+    _launch(dev, "nq_kv_plan", (cached_p, new_p, table_p, ld, width, free_p, n_free, head_p, out_p, cu_p,
+                                cu_p + 4 * (B + 1), cu_p + 4 * (2 * B + 2), slots.data_ptr(), B, tokens, page_size, flags),
+            stream)
     return cu_q, kv_lens, positions, slots, free_head_out
 
 
@@ -595,36 +619,31 @@ def nq_kv_append_nvfp4(k, v, slots, cache, k_scale, v_scale, *, flags: int = 0, 
     """Quantize keys and values (bf16 [T, kv heads, d], any token and head strides) into
     their slots (int64 [T], < 0 skips) of ``cache`` (uint8 of ``kv_cache_shape``), under
     the one-element float32 global scales ``k_scale`` and ``v_scale``."""
-    T, H, d, kt, kh = _heads(k, "k")
-    Tv, _, _, vt, vh = _heads(v, "v", d, H)
-    _need(Tv == T, f"v must have {T} tokens")
-    pages, heads, page, stride = _cache(cache, d)
+    dev = _device(k, "k")
+    T, H, d, kt, kh, k_p = _heads(k, "k", dev)
+    _, _, _, vt, vh, v_p = _heads(v, "v", dev, T, H, d)
+    pages, heads, page, stride, cache_p = _cache(cache, d, dev)
     _need(heads == H, f"cache has {heads} kv heads, k has {H}")
-    _ints(slots, "slots", torch.int64, T)
-    _scalar(k_scale, "k_scale")
-    _scalar(v_scale, "v_scale")
-    _same_device(k, v, slots, cache, k_scale, v_scale)
-    _launch(k.device, "nq_kv_append_nvfp4", k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, slots.data_ptr(),
-            k_scale.data_ptr(), v_scale.data_ptr(), cache.data_ptr(), stride, pages, T, H, d, page, flags, stream=stream)
+    _, slots_p = _vector(slots, "slots", torch.int64, T, dev)
+    _launch(dev, "nq_kv_append_nvfp4", (k_p, kt, kh, v_p, vt, vh, slots_p, _one(k_scale, "k_scale", dev),
+                                        _one(v_scale, "v_scale", dev), cache_p, stride, pages, T, H, d, page, flags), stream)
 
 
 def nq_kv_gather_nvfp4(cache, slots, k_scale, v_scale, head_dim: int, *, k_out=None, v_out=None, flags: int = 0,
                        stream=None):
     """Read tokens back: ``(k, v)`` bf16 [T, kv heads, head_dim] of ``slots`` (int64 [T], < 0 gives zeros)."""
-    pages, H, page, stride = _cache(cache, head_dim)
-    _need(isinstance(slots, torch.Tensor) and slots.dim() == 1, "slots must be an int64 CUDA tensor [T]")
-    T = slots.shape[0]
-    _ints(slots, "slots", torch.int64, T)
-    _scalar(k_scale, "k_scale")
-    _scalar(v_scale, "v_scale")
-    k_out = _out(k_out, (T, H, head_dim), torch.bfloat16, cache, "k_out")
-    v_out = _out(v_out, (T, H, head_dim), torch.bfloat16, cache, "v_out")
-    _, _, _, kt, kh = _heads(k_out, "k_out")
-    _, _, _, vt, vh = _heads(v_out, "v_out")
-    _same_device(cache, slots, k_scale, v_scale, k_out, v_out)
-    _launch(cache.device, "nq_kv_gather_nvfp4", cache.data_ptr(), stride, pages, slots.data_ptr(), k_scale.data_ptr(),
-            v_scale.data_ptr(), k_out.data_ptr(), kt, kh, v_out.data_ptr(), vt, vh, T, H, head_dim, page, flags,
-            stream=stream)
+    dev = _device(cache, "cache")
+    pages, H, page, stride, cache_p = _cache(cache, head_dim, dev)
+    T, slots_p = _vector(slots, "slots", torch.int64, None, dev)
+    if k_out is None:
+        k_out = torch.empty((T, H, head_dim), dtype=torch.bfloat16, device=cache.device)
+    if v_out is None:
+        v_out = torch.empty((T, H, head_dim), dtype=torch.bfloat16, device=cache.device)
+    _, _, _, kt, kh, k_p = _heads(k_out, "k_out", dev, T, H, head_dim)
+    _, _, _, vt, vh, v_p = _heads(v_out, "v_out", dev, T, H, head_dim)
+    _launch(dev, "nq_kv_gather_nvfp4", (cache_p, stride, pages, slots_p, _one(k_scale, "k_scale", dev),
+                                        _one(v_scale, "v_scale", dev), k_p, kt, kh, v_p, vt, vh, T, H, head_dim, page, flags),
+            stream)
     return k_out, v_out
 
 
@@ -642,36 +661,30 @@ def nq_attention_nvfp4_kv(q, cache, block_table, kv_lens, cu_q, k_scale, v_scale
     without it each call makes its own.  Returns ``(out bf16 [T, heads, d], lse
     float32 [T, heads] or None)``; rows no request owns are left as they were.
     """
-    T, heads, d, qt, qh = _heads(q, "q")
-    pages, H, page, stride = _cache(cache, d)
-    _need(isinstance(kv_lens, torch.Tensor) and kv_lens.dim() == 1, "kv_lens must be an int32 CUDA tensor [B]")
-    B = kv_lens.shape[0]
-    _ints(kv_lens, "kv_lens", torch.int32, B)
-    _ints(cu_q, "cu_q", torch.int32, B + 1)
-    width, ld = _table(block_table, B)
-    _scalar(k_scale, "k_scale")
-    _scalar(v_scale, "v_scale")
+    dev = _device(q, "q")
+    T, heads, d, qt, qh, q_p = _heads(q, "q", dev)
+    pages, H, page, stride, cache_p = _cache(cache, d, dev)
+    B, kv_p = _vector(kv_lens, "kv_lens", torch.int32, None, dev)
+    _, cu_p = _vector(cu_q, "cu_q", torch.int32, B + 1, dev)
+    width, ld, table_p = _table(block_table, B, dev)
     if out is None:
         out = torch.empty((T, heads, d), dtype=torch.bfloat16, device=q.device)
-        ot, oh = heads * d, d
+        ot, oh, out_p = heads * d, d, out.data_ptr()
     else:
-        To, _, _, ot, oh = _heads(out, "out", d, heads)
-        _need(To == T, f"out must have {T} tokens")
+        _, _, _, ot, oh, out_p = _heads(out, "out", dev, T, heads, d)
     if want_lse and lse is None:
         lse = torch.empty((T, heads), dtype=torch.float32, device=q.device)
-    ld_lse = heads
+    lse_p, ld_lse = None, heads
     if lse is not None:
-        _need(isinstance(lse, torch.Tensor) and lse.is_cuda and lse.dtype == torch.float32 and lse.shape == (T, heads)
-              and (heads <= 1 or lse.stride(1) == 1), f"lse must be a float32 CUDA tensor {(T, heads)}")
-        ld_lse = lse.stride(0) if T > 1 else max(lse.stride(0), heads)
+        _need(isinstance(lse, torch.Tensor) and lse.dtype is torch.float32 and lse.shape == (T, heads)
+              and lse.get_device() == dev and (heads <= 1 or lse.stride(1) == 1),
+              f"lse must be a float32 tensor {(T, heads)} on cuda:{dev}")
+        lse_p, ld_lse = lse.data_ptr(), (lse.stride(0) if T > 1 else max(lse.stride(0), heads))
     if workspace is None:
         workspace = torch.zeros(ATTENTION_WORKSPACE_BYTES, dtype=torch.uint8, device=q.device)
-    _need(isinstance(workspace, torch.Tensor) and workspace.is_cuda and workspace.dtype == torch.uint8
-          and workspace.dim() == 1 and (workspace.shape[0] <= 1 or workspace.stride(0) == 1),
-          "workspace must be a contiguous uint8 CUDA tensor")
-    _same_device(q, cache, block_table, kv_lens, cu_q, k_scale, v_scale, out, lse, workspace)
-    _launch(q.device, "nq_attention_nvfp4_kv", q.data_ptr(), qt, qh, cache.data_ptr(), stride, pages,
-            block_table.data_ptr(), ld, width, kv_lens.data_ptr(), cu_q.data_ptr(), k_scale.data_ptr(),
-            v_scale.data_ptr(), out.data_ptr(), ot, oh, _ptr(lse), ld_lse, workspace.data_ptr(), workspace.shape[0], T, B,
-            heads, H, d, page, d ** -0.5 if scale is None else scale, window, flags, stream=stream)
+    ws_n, ws_p = _vector(workspace, "workspace", torch.uint8, None, dev)
+    _launch(dev, "nq_attention_nvfp4_kv",
+            (q_p, qt, qh, cache_p, stride, pages, table_p, ld, width, kv_p, cu_p, _one(k_scale, "k_scale", dev),
+             _one(v_scale, "v_scale", dev), out_p, ot, oh, lse_p, ld_lse, ws_p, ws_n, T, B, heads, H, d, page,
+             d ** -0.5 if scale is None else scale, window, flags), stream)
     return out, lse
