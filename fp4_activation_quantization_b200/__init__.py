@@ -656,9 +656,9 @@ def nq_attention_nvfp4_kv(q, cache, block_table, kv_lens, cu_q, k_scale, v_scale
     (int32 [B + 1]), the last ones of its ``kv_lens[b]`` tokens (int32 [B]), whose
     pages ``block_table`` (int32 [B, pages]) lists.  Causal unless ``flags`` has
     FLAG_NONCAUSAL; ``window`` > 0 limits a row to its last ``window`` keys;
-    ``scale`` defaults to d ** -0.5.  ``workspace``: a zero-filled uint8 CUDA
-    tensor of ATTENTION_WORKSPACE_BYTES, kept between calls (one per stream);
-    without it each call makes its own.  Returns ``(out bf16 [T, heads, d], lse
+    ``scale`` defaults to d ** -0.5.  ``workspace``: a zero-filled uint8
+    CUDA tensor of ATTENTION_WORKSPACE_BYTES, kept between calls that do not run
+    at the same time; without it each call makes its own.  Returns ``(out bf16 [T, heads, d], lse
     float32 [T, heads] or None)``; rows no request owns are left as they were.
     """
     dev = _device(q, "q")

@@ -20,11 +20,22 @@
 // its 8-column side.  Bound by HBM in the limit: an atom of D = 128 is 2304
 // bytes and costs a warp about 250 instructions.
 //
-// Split.  The tokens of all (request, kv head) pairs form one axis of units of
-// 64 tokens; every CTA takes an equal share of it, whatever the lengths.  A
-// segment cut by a CTA's boundary leaves its unnormalised result in the
-// workspace, and the CTA that arrives last joins them in the order of the
-// tokens, so results do not depend on timing.  No CTA waits for another.
+// Split.  The atoms of all (request, row tile, kv head) segments form one axis,
+// which is shared out equally whatever the lengths, in one of two ways:
+//  - many segments (WALK): every warp takes a contiguous share and walks the
+//    segments in it on its own, without a barrier, so that one warp's change of
+//    segment (five dependent loads) passes under the others' work.  A segment
+//    inside one share is written out by its warp; the parts of one that is cut
+//    go to the workspace, and a second launch, which starts under the first
+//    one's end, joins them.
+//  - few segments: every CTA takes one chunk of one segment, of 32 atoms or more,
+//    its warps a quarter each; they are joined in shared memory, and the CTA
+//    that arrives last at a segment's counter joins its chunks.  One launch: a
+//    second one costs as much as a short context takes.
+// Parts are joined in the order of the tokens, so results do not depend on
+// timing.  No CTA waits for another.
+// (The first way by CTAs instead of warps: every segment cost 5 us of loads,
+// barriers and fences; 128 ragged requests 172 us.)
 #include "nq_kv_layout.cuh"
 
 namespace nq {
@@ -32,8 +43,8 @@ namespace nq {
 namespace {
 
 constexpr int kWarps = kAttnRowsThreads / 32;
-constexpr int kUnit = 16 * kWarps;  // tokens of a unit: one atom per warp
 constexpr float kRaise = 8.0f;      // log2 by which a score may exceed the running maximum
+constexpr float kLowest = -3.0e38f; // the maximum of no scores: below every finite one, and 0 * 2^(kLowest - kLowest) is 0
 
 constexpr int stages_of(int d) { return d == 256 ? 3 : 4; }
 constexpr size_t ring_bytes(int d) { return size_t(kWarps) * stages_of(d) * 18 * d; }
@@ -63,18 +74,24 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
   return d;
 }
+// first: the accumulator starts from zero.
 __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                    uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+                                    uint32_t b1, bool first = false) {
+  if (first)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+                 : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 // One request's share of the axis.
 struct Span {
   int q0, q_len, kv_len;  // first query row, rows, keys
   int first;              // first key any row sees, rounded down to an atom
-  int tiles, units;       // row tiles; units of keys per tile and kv head
+  int tiles, units;       // row tiles; atoms of keys per tile and kv head
 };
 template <int R>
 __device__ __forceinline__ Span span_of(const AttnArgs& a, int b) {
@@ -87,21 +104,145 @@ __device__ __forceinline__ Span span_of(const AttnArgs& a, int b) {
   s.first = 0;
   if (a.window > 0) s.first = int(max(int64_t(0), int64_t(s.kv_len) - s.q_len + 1 - a.window)) & ~15;
   s.tiles = int((int64_t(s.q_len) * a.group + R - 1) / R);
-  s.units = max(1, (s.kv_len - s.first + kUnit - 1) / kUnit);
+  s.units = max(1, (s.kv_len - s.first + 15) >> 4);
   return s;
 }
 
-template <int D, int NT>
-__global__ void __launch_bounds__(kAttnRowsThreads, D == 256 ? 2 : (NT == 1 ? 4 : 3)) rows_kernel(const AttnArgs a) {
+// What the joining launch needs to know of a segment whose first part is p.
+struct __align__(16) Cut {
+  int32_t valid, q0, row0, rows;   // first query row of the request, first row and rows of the tile
+  int32_t head, last, pad0, pad1;  // kv head, last part
+};
+// The workspace: counters of the chunked segments (zero between calls); for the
+// walk [0] the number of parts and, from there on, the cuts; then the parts'
+// slots, each of R rows of D floats and R pairs (maximum, sum).
+__device__ __forceinline__ uint32_t* counters_of(const AttnArgs& a) { return reinterpret_cast<uint32_t*>(a.workspace); }
+__device__ __forceinline__ int32_t* parts_of(const AttnArgs& a) {
+  return reinterpret_cast<int32_t*>(a.workspace + kAttnCounterBytes);
+}
+__device__ __forceinline__ Cut* cuts_of(const AttnArgs& a) {
+  return reinterpret_cast<Cut*>(a.workspace + kAttnCounterBytes + 64);
+}
+template <int D, int R>
+__device__ __forceinline__ float* slot_of(const AttnArgs& a, int64_t i) {
+  return reinterpret_cast<float*>(a.workspace + kAttnHeader) + i * (R * (D + 2));
+}
+
+__device__ __forceinline__ void store_pair(uint16_t* op, float x0, float x1) {
+  const uint32_t v = pack_bf16x2(x0, x1);
+  if ((reinterpret_cast<uintptr_t>(op) & 3) == 0) {
+    *reinterpret_cast<uint32_t*>(op) = v;
+  } else {
+    op[0] = uint16_t(v);
+    op[1] = uint16_t(v >> 16);
+  }
+}
+__device__ __forceinline__ float out_factor(float sum, float gv) { return sum > 0.0f || sum != sum ? gv / sum : 0.0f; }
+__device__ __forceinline__ float lse_of(float top, float sum) {
+  return sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+}
+
+// Joins n parts of a tile (part p at slot(p)), in order, with THREADS threads of a
+// CTA, and writes the rows out.  Weights first, then the rows in independent
+// loads: one dependent load a part would cost 0.7 us each.
+template <int D, int R, int THREADS>
+struct Join {
+  static constexpr int kMax = 64;  // parts at a time
+  float weight[kMax * R], sum[kMax * R], top[R], l[R], f[R];
+
+  template <typename Slot>
+  __device__ __forceinline__ void run(const AttnArgs& a, int n, Slot&& slot, const Cut& cut, float gv) {
+    constexpr int kE = (R * D / 4 + THREADS - 1) / THREADS;
+    constexpr int kBatch = kE >= 16 ? 1 : 16 / kE;  // parts whose rows are on their way together
+    const int tid = int(threadIdx.x);
+    float4 x[kE];
+#pragma unroll
+    for (int e = 0; e < kE; ++e) x[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (tid < R) top[tid] = kLowest, l[tid] = 0.0f;
+    for (int p0 = 0; p0 < n; p0 += kMax) {
+      const int here = min(kMax, n - p0);
+      __syncthreads();
+      for (int i = tid; i < here * R; i += THREADS) {
+        const int row = i % R;
+        const float2 st = row < cut.rows ? __ldcg(reinterpret_cast<const float2*>(slot(p0 + i / R) + R * D + 2 * row))
+                                         : make_float2(kLowest, 0.0f);
+        weight[i] = st.x;
+        sum[i] = st.y;
+      }
+      __syncthreads();
+      if (tid < R) {
+        float m = top[tid];
+#pragma unroll 8
+        for (int p = 0; p < here; ++p) m = fmaxf(m, weight[p * R + tid]);
+        const float g = ex2(top[tid] - m);
+        float s = l[tid] * g;
+#pragma unroll 8
+        for (int p = 0; p < here; ++p) {
+          const float w = ex2(weight[p * R + tid] - m);
+          weight[p * R + tid] = w;
+          s += w * sum[p * R + tid];
+        }
+        top[tid] = m;
+        l[tid] = s;
+        f[tid] = g;
+      }
+      __syncthreads();
+#pragma unroll
+      for (int e = 0; e < kE; ++e) {
+        const int row = (e * THREADS + tid) / (D / 4);
+        const float g = row < R ? f[row] : 0.0f;
+        x[e] = make_float4(x[e].x * g, x[e].y * g, x[e].z * g, x[e].w * g);
+      }
+      for (int p = 0; p < here; p += kBatch) {
+        float4 v[kBatch][kE];
+#pragma unroll
+        for (int q = 0; q < kBatch; ++q)
+#pragma unroll
+          for (int e = 0; e < kE; ++e) {
+            const int i = e * THREADS + tid, row = i / (D / 4);
+            v[q][e] = p + q < here && row < cut.rows
+                          ? __ldcg(reinterpret_cast<const float4*>(slot(p0 + p + q) + row * D + 4 * (i % (D / 4))))
+                          : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          }
+#pragma unroll
+        for (int q = 0; q < kBatch; ++q)
+#pragma unroll
+          for (int e = 0; e < kE; ++e) {
+            const int row = (e * THREADS + tid) / (D / 4);
+            if (p + q < here && row < cut.rows) {
+              const float w = weight[(p + q) * R + row];
+              x[e] = make_float4(x[e].x + w * v[q][e].x, x[e].y + w * v[q][e].y, x[e].z + w * v[q][e].z,
+                                 x[e].w + w * v[q][e].w);
+            }
+          }
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < kE; ++e) {
+      const int i = e * THREADS + tid, row = i / (D / 4), d = 4 * (i % (D / 4));
+      if (row >= cut.rows) continue;
+      const int y = cut.row0 + row, token = y / a.group, h = cut.head * a.group + y - token * a.group;
+      const int64_t at = cut.q0 + token;
+      const float g = out_factor(l[row], gv);
+      uint16_t* op = a.out + at * a.ld_ot + h * a.ld_oh + d;
+      store_pair(op, x[e].x * g, x[e].y * g);
+      store_pair(op + 2, x[e].z * g, x[e].w * g);
+      if (a.lse != nullptr && d == 0) a.lse[at * a.ld_lse + h] = lse_of(top[row], l[row]);
+    }
+  }
+};
+
+template <int D, int NT, bool WALK>
+__global__ void __launch_bounds__(kAttnRowsThreads, D == 256 ? 2 : (NT == 1 ? 4 : (NT == 2 ? 3 : 2)))
+    rows_kernel(const AttnArgs a) {
   constexpr int R = 8 * NT;  // rows of a tile: (token, head of the group), token-major
   constexpr int kStages = stages_of(D);
   constexpr int kN = KvAtom<D>::kN, kW = KvAtom<D>::kW;
   constexpr int kAtom = KvAtom<D>::kBytes;
   constexpr int kPitch = row_pitch(D);
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int64_t s_scan[2][kWarps];
-  __shared__ int64_t s_found[3];
-  __shared__ int s_last;
+  __shared__ int64_t s_scan[kWarps], s_base[kWarps];
+  __shared__ int s_req[kWarps], s_last;
 
   const int tid = int(threadIdx.x), lane = tid & 31, warp = tid >> 5;
   const int r = lane >> 2, j = lane & 3;
@@ -110,72 +251,191 @@ __global__ void __launch_bounds__(kAttnRowsThreads, D == 256 ? 2 : (NT == 1 ? 4 
   griddep_wait();
   griddep_launch_dependents();
 
-  // ---- the axis: units and segments of all requests, and the request of this CTA's first unit
+  // ---- the axis: atoms of all requests (each thread counts a run of them)
   const int per = (a.B + kAttnRowsThreads - 1) / kAttnRowsThreads;
   const int b_lo = min(a.B, tid * per), b_hi = min(a.B, b_lo + per);
-  int64_t mine = 0, segs = 0;
+  // Sum of `mine` over the CTA's threads, and over those before this one.
+  auto scan = [&](int64_t mine, int64_t* before) {
+    int64_t incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t up = __shfl_up_sync(kFull, incl, o);
+      if (lane >= o) incl += up;
+    }
+    __syncthreads();
+    if (lane == 31) s_scan[warp] = incl;
+    __syncthreads();
+    int64_t total = 0;
+    *before = incl - mine;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) *before += s_scan[w];
+      total += s_scan[w];
+    }
+    return total;
+  };
+  int64_t mine = 0, segments = 0, before;
   for (int b = b_lo; b < b_hi; ++b) {
     const Span s = span_of<R>(a, b);
     mine += int64_t(s.tiles) * heads * s.units;
-    segs += int64_t(s.tiles) * heads;
+    segments += int64_t(s.tiles) * heads;
   }
-  int64_t incl = mine, segs_all = segs;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t up = __shfl_up_sync(kFull, incl, o);
-    if (lane >= o) incl += up;
-    segs_all += __shfl_xor_sync(kFull, segs_all, o);
-  }
-  if (lane == 31) s_scan[0][warp] = incl, s_scan[1][warp] = segs_all;
-  __syncthreads();
-  int64_t total = 0, before = incl - mine;
-  segs_all = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) before += s_scan[0][w];
-    total += s_scan[0][w];
-    segs_all += s_scan[1][w];
-  }
-  if (total == 0) return;
-  // CTAs that take part: at most one per unit, and at most max_splits per segment on average.
-  const int64_t parts = min(int64_t(gridDim.x), min(total, segs_all * a.max_splits));
-  if (int64_t(blockIdx.x) >= parts) return;
-  const int64_t u0 = total * blockIdx.x / parts, u1 = total * (blockIdx.x + 1) / parts;
-  auto part_of = [&](int64_t u) { return int(((u + 1) * parts - 1) / total); };  // the CTA that owns unit u
-  if (mine > 0 && u0 >= before && u0 < before + mine) {
-    int64_t at = before;
-    int b = b_lo;
-    for (; b < b_hi; ++b) {
+  int64_t total = scan(mine, &before);
+
+  // WALK: shares of the axis, one a warp, of two atoms or more; few shares go to
+  // a warp of every CTA first.  Else: chunks of `chunk` atoms that no segment
+  // shares, one a CTA.
+  int parts = 0, chunk = 0;
+  auto part_of_warp = [&](int w) {
+    return parts == int(gridDim.x) * kWarps ? int(blockIdx.x) * kWarps + w : w * int(gridDim.x) + int(blockIdx.x);
+  };
+  auto start_of = [&](int64_t p) { return total * p / parts; };
+  auto owner_of = [&](int64_t u) { return int(((u + 1) * parts - 1) / total); };
+  if constexpr (WALK) {
+    parts = int(min(int64_t(gridDim.x) * kWarps, (total + 1) >> 1));
+    if (blockIdx.x == 0 && tid == 0) *parts_of(a) = parts;
+  } else {
+    int64_t unused;
+    const int64_t all = scan(segments, &unused);
+    // Sum over the segments of ceil(atoms / chunk) stays within the grid.
+    const int64_t free = int64_t(gridDim.x) - all;
+    chunk = int(max(int64_t(32), free > 0 ? (total + free - 1) / free : total));
+    mine = 0;
+    for (int b = b_lo; b < b_hi; ++b) {
       const Span s = span_of<R>(a, b);
-      const int64_t n = int64_t(s.tiles) * heads * s.units;
-      if (u0 < at + n) break;
-      at += n;
+      mine += int64_t(s.tiles) * heads * ((s.units + chunk - 1) / chunk);
     }
-    s_found[0] = b;
-    s_found[1] = at;
+    total = scan(mine, &before);
+  }
+  auto units_of = [&](const Span& s) { return WALK ? s.units : (s.units + chunk - 1) / chunk; };  // of the axis, per segment
+  if (mine > 0) {
+#pragma unroll
+    for (int w = 0; w < (WALK ? kWarps : 1); ++w) {
+      const int p = WALK ? part_of_warp(w) : int(blockIdx.x);
+      if (WALK && p >= parts) continue;
+      const int64_t u = WALK ? start_of(p) : p;
+      if (u < before || u >= before + mine) continue;
+      int64_t at = before;
+      int b = b_lo;
+      for (; b < b_hi; ++b) {
+        const Span s = span_of<R>(a, b);
+        const int64_t n = int64_t(s.tiles) * heads * units_of(s);
+        if (u < at + n) break;
+        at += n;
+      }
+      s_req[w] = b;
+      s_base[w] = at;
+    }
   }
   __syncthreads();
-  int b = int(s_found[0]);
-  int64_t base = s_found[1];  // first unit of request b
+  int part = WALK ? part_of_warp(warp) : int(blockIdx.x);
+  int64_t u0 = 0, u1 = 0;  // this warp's (CTA's) share of the axis
+  if constexpr (WALK) {
+    if (part < parts) u0 = start_of(part), u1 = start_of(part + 1);
+  } else {
+    if (part >= total) return;
+    u0 = part, u1 = part + 1;
+  }
+  int b = s_req[WALK ? warp : 0];
+  int64_t base = s_base[WALK ? warp : 0];  // where request b begins on the axis
 
   const uint32_t ring = uint32_t(__cvta_generic_to_shared(smem)) + warp * (kStages * kAtom);
   const uint8_t* ring_p = smem + warp * (kStages * kAtom);
   const float gk = __ldg(a.k_scale), gv = __ldg(a.v_scale);
   const int64_t head_bytes = int64_t(kAtom) << (a.cache.log_page - 4);
+  Cut cut{};
 
   int64_t u = u0;
   while (u < u1) {
     Span s = span_of<R>(a, b);
-    while (base + int64_t(s.tiles) * heads * s.units <= u) {  // the next request that has rows
-      base += int64_t(s.tiles) * heads * s.units;
+    while (base + int64_t(s.tiles) * heads * units_of(s) <= u) {  // the next request that has rows
+      base += int64_t(s.tiles) * heads * units_of(s);
       s = span_of<R>(a, ++b);
     }
-    // ---- segment (request b, row tile, kv head): units [ua, ub) of it are ours
-    const int64_t seg = (u - base) / s.units;
-    const int64_t seg0 = base + seg * s.units;
-    const int head = int(seg % heads), tile = int(seg / heads);
-    const int ua = int(u - seg0), ub = int(min(u1 - seg0, int64_t(s.units)));
+    // ---- segment (request b, row tile, kv head): atoms [ua, ub) of it are this warp's
+    const int units = units_of(s);
+    const int64_t seg = (u - base) / units;
+    const int64_t seg0 = base + seg * units;
+    const int tile = int(seg / heads), head = int(seg - int64_t(tile) * heads);
     const int rows = min(R, s.q_len * a.group - tile * R);
+    int ua, ub;
+    if constexpr (WALK) {
+      ua = int(u - seg0);
+      ub = int(min(u1 - seg0, int64_t(units)));
+    } else {
+      const int c0 = int(u - seg0) * chunk, n = min(chunk, s.units - c0);
+      ua = c0 + n * warp / kWarps;
+      ub = c0 + n * (warp + 1) / kWarps;
+    }
+
+    // Keys in sight of columns 2j and 2j + 1 of each 8-row tile.
+    int lo[NT][2], hi[NT][2];
+    int lo_all = 0x7fffffff, hi_all = 0;    // union and ...
+    int lo_full = 0, hi_full = 0x7fffffff;  // ... intersection over the tile's rows
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int row = nt * 8 + 2 * j + i;
+        lo[nt][i] = 0;
+        hi[nt][i] = 0;
+        if (row < rows) {
+          const int64_t pos = int64_t(s.kv_len) - s.q_len + (tile * R + row) / a.group;
+          hi[nt][i] = a.causal ? int(min(int64_t(s.kv_len), max(int64_t(0), pos + 1))) : s.kv_len;
+          lo[nt][i] = a.window > 0 ? int(max(int64_t(0), pos + 1 - a.window)) : 0;
+          lo_all = min(lo_all, lo[nt][i]);
+          hi_all = max(hi_all, hi[nt][i]);
+          lo_full = max(lo_full, lo[nt][i]);
+          hi_full = min(hi_full, hi[nt][i]);
+        }
+      }
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) {
+      lo_all = min(lo_all, __shfl_xor_sync(kFull, lo_all, o));
+      hi_all = max(hi_all, __shfl_xor_sync(kFull, hi_all, o));
+      lo_full = max(lo_full, __shfl_xor_sync(kFull, lo_full, o));
+      hi_full = min(hi_full, __shfl_xor_sync(kFull, hi_full, o));
+    }
+
+    // ---- the atoms of the share that some row sees; the first ones are on their way from here
+    const int t0 = max(s.first + 16 * ua, lo_all & ~15), t1 = min(s.first + 16 * ub, hi_all);
+    const int n_atoms = t0 < t1 ? (t1 - t0 + 15) >> 4 : 0;
+    const int32_t* table = a.table + int64_t(b) * a.ld_table;
+    const uint8_t* const base_lane = a.cache.base + head * head_bytes + 16 * lane;
+    const int page_atoms = 1 << (a.cache.log_page - 4);
+    // Atoms are issued in order: within a page the source only moves on.
+    int page_i = (t0 >> a.cache.log_page) - 1, page_end = n_atoms > 0 ? (t1 - 1) >> a.cache.log_page : -1;
+    auto page_at = [&](int i) { return i <= page_end ? __ldg(table + i) : 0; };
+    int next_page = page_at(page_i + 1), left = 0, to_issue = n_atoms;
+    const uint8_t* src = nullptr;
+    bool gone = false;
+    uint32_t missing = 0, dst = ring + 16 * lane;  // missing, bit i: the atom issued i + 1 calls ago has no page
+    auto issue = [&]() {
+      if (to_issue > 0) {
+        if (left == 0) {
+          const int in = page_end >= 0 && src == nullptr ? (t0 >> 4) & (page_atoms - 1) : 0;
+          gone = uint32_t(next_page) >= uint32_t(a.cache.pages);
+          src = base_lane + int64_t(next_page) * a.cache.page_stride + in * kAtom;
+          left = page_atoms - in;
+          ++page_i;
+          next_page = page_at(page_i + 1);
+        }
+        if (!gone) {
+#pragma unroll
+          for (int x = 0; x < (kAtom / 16 + 31) / 32; ++x)
+            if (kAtom / 16 % 32 == 0 || x * 32 + lane < kAtom / 16) cp_async16(dst + 512 * x, src + 512 * x);
+        }
+        src += kAtom;
+        --left;
+        --to_issue;
+      }
+      missing = missing << 1 | (gone ? 1u : 0u);
+      dst += kAtom;
+      if (dst >= ring + kStages * kAtom) dst -= kStages * kAtom;
+      cp_async_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) issue();
 
     // Query fragments: lane (n = r, j) holds row n's dimensions [j D/4, (j+1) D/4) of each 8-row tile.
     uint32_t qf[NT][D / 16][2];
@@ -215,8 +475,10 @@ __global__ void __launch_bounds__(kAttnRowsThreads, D == 256 ? 2 : (NT == 1 ? 4 
       amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 2));
       const int e = int(__float_as_uint(amax) >> 23) - 127;
       const int k = (amax == 0.0f || e > 127) ? 0 : min(14 - e, 100);
-      const float up = __uint_as_float(uint32_t(k + 127) << 23), down = __uint_as_float(uint32_t(127 - k) << 23);
-      c_row[nt] = a.scale_log2 * gk * down;
+      const float factor = a.scale_log2 * gk;
+      const float up = copysignf(__uint_as_float(uint32_t(k + 127) << 23), factor);
+      // At least the smallest normal number: 0 would make NaN of a masked key's -inf.
+      c_row[nt] = fmaxf(fabsf(factor) * __uint_as_float(uint32_t(127 - k) << 23), 1.17549435e-38f);
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) {
         float v[8];
@@ -225,38 +487,15 @@ __global__ void __launch_bounds__(kAttnRowsThreads, D == 256 ? 2 : (NT == 1 ? 4 
         for (int e2 = 0; e2 < 4; ++e2) qf[nt][2 * i + (e2 >> 1)][e2 & 1] = pack_f16x2(v[2 * e2] * up, v[2 * e2 + 1] * up);
       }
     }
-    // Columns 2j and 2j + 1 of each tile: score factor, keys in sight.
-    float cs[NT][2], m[NT][2], l[NT][2];
-    int lo[NT][2], hi[NT][2];
-    int lo_all = 0x7fffffff, hi_all = 0;    // union and ...
-    int lo_full = 0, hi_full = 0x7fffffff;  // ... intersection over the tile's rows
+    float cs[NT][2], m[NT][2], l[NT][2];  // columns 2j and 2j + 1: score factor, maximum, sum of this lane's weights
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int row = nt * 8 + 2 * j + i;
         cs[nt][i] = __shfl_sync(kFull, c_row[nt], 4 * (2 * j + i));
-        m[nt][i] = -INFINITY;
+        m[nt][i] = kLowest;
         l[nt][i] = 0.0f;
-        lo[nt][i] = 0;
-        hi[nt][i] = 0;
-        if (row < rows) {
-          const int64_t pos = int64_t(s.kv_len) - s.q_len + (tile * R + row) / a.group;
-          hi[nt][i] = a.causal ? int(min(int64_t(s.kv_len), max(int64_t(0), pos + 1))) : s.kv_len;
-          lo[nt][i] = a.window > 0 ? int(max(int64_t(0), pos + 1 - a.window)) : 0;
-          lo_all = min(lo_all, lo[nt][i]);
-          hi_all = max(hi_all, hi[nt][i]);
-          lo_full = max(lo_full, lo[nt][i]);
-          hi_full = min(hi_full, hi[nt][i]);
-        }
       }
-#pragma unroll
-    for (int o = 1; o < 4; o <<= 1) {
-      lo_all = min(lo_all, __shfl_xor_sync(kFull, lo_all, o));
-      hi_all = max(hi_all, __shfl_xor_sync(kFull, hi_all, o));
-      lo_full = max(lo_full, __shfl_xor_sync(kFull, lo_full, o));
-      hi_full = min(hi_full, __shfl_xor_sync(kFull, hi_full, o));
-    }
     float o[D / 16][NT][4];
 #pragma unroll
     for (int mt = 0; mt < D / 16; ++mt)
@@ -265,64 +504,19 @@ __global__ void __launch_bounds__(kAttnRowsThreads, D == 256 ? 2 : (NT == 1 ? 4 
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[mt][nt][i] = 0.0f;
 
-    // ---- this warp's atoms: first + 16 * (kWarps * unit + warp), those in sight of some row
-    int t0 = s.first + kUnit * ua + 16 * warp;
-    int t1 = s.first + kUnit * ub;
-    {
-      const int lo_atom = lo_all & ~15;
-      if (t0 < lo_atom) t0 += (lo_atom - t0 + kUnit - 1) / kUnit * kUnit;
-      t1 = min(t1, hi_all);
-    }
-    const int n_atoms = t0 < t1 ? (t1 - t0 + kUnit - 1) / kUnit : 0;
-    const int32_t* table = a.table + int64_t(b) * a.ld_table;
-    uint32_t missing = 0;  // bit i: the atom issued i + 1 calls ago has no page
-    auto issue = [&](int i) {
-      bool gone = false;
-      if (i < n_atoms) {
-        const int t = t0 + i * kUnit;
-        const int page = __ldg(table + (t >> a.cache.log_page));
-        gone = page < 0 || page >= a.cache.pages;
-        if (!gone) {
-          const uint8_t* src = a.cache.base + page * a.cache.page_stride + head * head_bytes +
-                               ((t & ((1 << a.cache.log_page) - 1)) >> 4) * kAtom;
-          const uint32_t dst = ring + (i % kStages) * kAtom;
-#pragma unroll
-          for (int x = 0; x < (kAtom / 16 + 31) / 32; ++x) {
-            const int c = x * 32 + lane;
-            if (kAtom / 16 % 32 == 0 || c < kAtom / 16) cp_async16(dst + 16 * c, src + 16 * c);
-          }
-        }
-      }
-      missing = (missing << 1) | (gone ? 1u : 0u);
-      cp_async_commit();
-    };
-#pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) issue(i);
-
-    for (int i = 0; i < n_atoms; ++i) {
-      cp_async_wait<kStages - 2>();
-      __syncwarp();  // all lanes' copies of atom i have landed, and all have read atom i - 1
-      const bool gone = (missing >> (kStages - 2)) & 1u;
-      issue(i + kStages - 1);
-      if (gone) {
-        if (lane == 0) atomicOr(a.err, kErrSlot);
-        continue;
-      }
-      const uint8_t* atom = ring_p + (i % kStages) * kAtom;
-      const int t = t0 + i * kUnit;
-
+    // One atom of 16 keys from t on; MASKED where some row does not see all of them.
+    auto step = [&](const uint8_t* atom, int t, auto masked_tag) {
+      constexpr bool MASKED = decltype(masked_tag)::value;
       // ---- S^T = K' q^T
       float sc[NT][4];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int x = 0; x < 4; ++x) sc[nt][x] = 0.0f;
       uint32_t ksw[(2 * kN + 3) / 4];  // the lane's 2 kN key scales
-      if constexpr (kN == 1) ksw[0] = *reinterpret_cast<const uint16_t*>(atom + KvAtom<D>::kKScales + lane * 2);
-      else
+      if constexpr (kN == 1) {
+        ksw[0] = *reinterpret_cast<const uint16_t*>(atom + KvAtom<D>::kKScales + lane * 2);
+      } else {
 #pragma unroll
         for (int x = 0; x < kN / 2; ++x)
           ksw[x] = *reinterpret_cast<const uint32_t*>(atom + KvAtom<D>::kKScales + lane * 2 * kN + 4 * x);
+      }
       uint32_t kw[2][kN][2];  // codes of rows r and r + 8
 #pragma unroll
       for (int pl = 0; pl < kN; ++pl) {
@@ -356,38 +550,46 @@ __global__ void __launch_bounds__(kAttnRowsThreads, D == 256 ? 2 : (NT == 1 ? 4 
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
               mma(sc[nt], ha[2 * y], hb[2 * y], ha[2 * y + 1], hb[2 * y + 1], qf[nt][4 * c + 2 * x + y][0],
-                  qf[nt][4 * c + 2 * x + y][1]);
+                  qf[nt][4 * c + 2 * x + y][1], c + x + y == 0);
         }
 
       // ---- softmax over the atom's tokens t + r (x = 0, 1) and t + r + 8 (x = 2, 3)
-      const bool masked = t < lo_full || t + 16 > hi_full;
+      if constexpr (MASKED) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int key = t + r + (x >> 1) * 8;
+            if (key < lo[nt][x & 1] || key >= hi[nt][x & 1]) sc[nt][x] = -INFINITY;
+          }
+      }
+      float arg[NT][4];  // log2 of the weights
       bool raise = false;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-          float v = sc[nt][x] * cs[nt][x & 1];
-          if (masked) {
-            const int key = t + r + (x >> 1) * 8;
-            if (key < lo[nt][x & 1] || key >= hi[nt][x & 1]) v = -INFINITY;
-          }
-          sc[nt][x] = v;
-          raise |= v > m[nt][x & 1] + kRaise;
+          arg[nt][x] = __fmaf_rn(sc[nt][x], cs[nt][x & 1], -m[nt][x & 1]);
+          raise |= arg[nt][x] > kRaise;
         }
       if (__any_sync(kFull, raise)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
-            float top = fmaxf(m[nt][y], fmaxf(sc[nt][y], sc[nt][y + 2]));
+            float top = fmaxf(sc[nt][y], sc[nt][y + 2]);
 #pragma unroll
             for (int w = 4; w < 32; w <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, w));
-            if (!(top > m[nt][y] + kRaise)) top = m[nt][y];  // a row's results do not depend on its neighbours'
-            const float f = top == m[nt][y] ? 1.0f : ex2(m[nt][y] - top);  // (-inf: both empty)
-            m[nt][y] = top;
-            l[nt][y] *= f;
+            if (__fmaf_rn(top, cs[nt][y], -m[nt][y]) > kRaise) {  // a row's results do not depend on its neighbours'
+              top *= cs[nt][y];
+              const float f = ex2(m[nt][y] - top);
+              m[nt][y] = top;
+              l[nt][y] *= f;
 #pragma unroll
-            for (int mt = 0; mt < D / 16; ++mt) o[mt][nt][y] *= f, o[mt][nt][y + 2] *= f;
+              for (int mt = 0; mt < D / 16; ++mt) o[mt][nt][y] *= f, o[mt][nt][y + 2] *= f;
+              arg[nt][y] = __fmaf_rn(sc[nt][y], cs[nt][y], -top);
+              arg[nt][y + 2] = __fmaf_rn(sc[nt][y + 2], cs[nt][y], -top);
+            }
           }
       }
       uint32_t pf[NT][2];
@@ -396,8 +598,7 @@ __global__ void __launch_bounds__(kAttnRowsThreads, D == 256 ? 2 : (NT == 1 ? 4 
         float p[4];
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-          const float top = m[nt][x & 1];
-          p[x] = ex2(sc[nt][x] - (top == -INFINITY ? 0.0f : top));
+          p[x] = ex2(arg[nt][x]);
           l[nt][x & 1] += p[x];
         }
         pf[nt][0] = transpose8x8(pack_f16x2(p[0], p[1]));
@@ -412,7 +613,7 @@ __global__ void __launch_bounds__(kAttnRowsThreads, D == 256 ? 2 : (NT == 1 ? 4 
         for (int x = 0; x < kW; ++x)
           w[x] = *reinterpret_cast<const uint32_t*>(atom + KvAtom<D>::kVScales +
                                                     ((D == 64 ? r >> 1 : r) * 4 + j) * (4 * kW) + 4 * x);
-        if (masked && t + 16 > s.kv_len) {
+        if (MASKED && t + 16 > s.kv_len) {
           // Bytes behind the last key are whatever the page held: their scales
           // become zero, so that 0 * NaN cannot reach the sum.
 #pragma unroll
@@ -432,8 +633,7 @@ __global__ void __launch_bounds__(kAttnRowsThreads, D == 256 ? 2 : (NT == 1 ? 4 
           }
         }
       }
-      // The lane's D/4 value bytes: words of 8 dimensions, D/64 * ... per token.
-      constexpr int kVW = D / 64;  // 32-bit words per token
+      constexpr int kVW = D / 64;  // 32-bit words of a lane's dimensions per token
       uint32_t vw[4][kVW];
 #pragma unroll
       for (int pl = 0; pl < kN; ++pl) {
@@ -463,119 +663,181 @@ __global__ void __launch_bounds__(kAttnRowsThreads, D == 256 ? 2 : (NT == 1 ? 4 
           for (int nt = 0; nt < NT; ++nt)
             mma(o[4 * x + y][nt], ev[0][y], od[0][y], ev[1][y], od[1][y], pf[nt][0], pf[nt][1]);
       }
+    };
+
+    // Atoms [i_lo, i_hi) are seen whole by every row.
+    const int i_lo = lo_full > t0 ? (lo_full - t0 + 15) >> 4 : 0;
+    const int i_hi = max(i_lo, hi_full > t0 ? (hi_full - t0) >> 4 : 0);
+    const uint8_t* atom = ring_p;
+    int t = t0;
+#pragma unroll 1
+    for (int i = 0; i < n_atoms; ++i) {
+      cp_async_wait<kStages - 2>();
+      __syncwarp();  // all lanes' copies of atom i have landed, and all have read atom i - 1
+      const bool absent = (missing >> (kStages - 2)) & 1u;
+      issue();
+      if (absent) {
+        if (lane == 0) atomicOr(a.err, kErrSlot);
+      } else if (uint32_t(i - i_lo) < uint32_t(i_hi - i_lo)) {
+        step(atom, t, BoolTag<false>{});
+      } else {
+        step(atom, t, BoolTag<true>{});
+      }
+      t += 16;
+      atom += kAtom;
+      if (atom == ring_p + kStages * kAtom) atom = ring_p;
     }
     cp_async_wait<0>();
+    __syncwarp();
 
-    // ---- join the warps: results per row in shared memory (over the ring)
-    __syncthreads();
-    float* res = reinterpret_cast<float*>(smem);                 // [kWarps][R][kPitch]
-    float* stat = res + kWarps * R * kPitch;                     // [kWarps][R][2]
+    // ---- the segment's end: sums over the lanes of a column
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        float sum = l[nt][y];
+      for (int y = 0; y < 2; ++y)
 #pragma unroll
-        for (int w = 4; w < 32; w <<= 1) sum += __shfl_xor_sync(kFull, sum, w);
-        const int row = nt * 8 + 2 * j + y;
-        float* rp = res + (warp * R + row) * kPitch + r * (D / 8);
+        for (int w = 4; w < 32; w <<= 1) l[nt][y] += __shfl_xor_sync(kFull, l[nt][y], w);
+    if constexpr (WALK) {
+      if (seg0 >= u0 && seg0 + units <= u1) {
 #pragma unroll
-        for (int mt = 0; mt < D / 16; ++mt)
-          *reinterpret_cast<float2*>(rp + 2 * mt) = make_float2(o[mt][nt][y], o[mt][nt][y + 2]);
-        if (r == 0) {
-          stat[(warp * R + row) * 2] = m[nt][y];
-          stat[(warp * R + row) * 2 + 1] = sum;
-        }
-      }
-    __syncthreads();
-    const int p_first = part_of(seg0), p_last = part_of(seg0 + s.units - 1);
-    const bool whole = p_first == p_last;
-    constexpr int kSlot = R * (D + 2);  // floats of a partial result: R rows of D, then R pairs (m, l)
-    float* slot = a.partials + (2 * int64_t(blockIdx.x) + (seg0 >= u0 ? 1 : 0)) * kSlot;
-    auto store_row = [&](int row, int d, float x0, float x1, float top, float sum) {
-      const int x = tile * R + row, token = x / a.group, g = x - token * a.group;
-      const int64_t at = s.q0 + token;
-      const int h = head * a.group + g;
-      const float f = sum > 0.0f || sum != sum ? gv / sum : 0.0f;
-      uint16_t* op = a.out + at * a.ld_ot + h * a.ld_oh + d;
-      const uint32_t v = pack_bf16x2(x0 * f, x1 * f);
-      if ((reinterpret_cast<uintptr_t>(op) & 3) == 0) {
-        *reinterpret_cast<uint32_t*>(op) = v;
-      } else {
-        op[0] = uint16_t(v);
-        op[1] = uint16_t(v >> 16);
-      }
-      if (a.lse != nullptr && d == 0)
-        a.lse[at * a.ld_lse + h] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
-    };
-    for (int i = tid; i < rows * (D / 2); i += kAttnRowsThreads) {
-      const int row = i / (D / 2), d = 2 * (i % (D / 2));
-      float top = -INFINITY;
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, stat[(w * R + row) * 2]);
-      float x0 = 0.0f, x1 = 0.0f, sum = 0.0f;
+          for (int y = 0; y < 2; ++y) {
+            const int row = nt * 8 + 2 * j + y;
+            if (row >= rows) continue;
+            const int x = tile * R + row, token = x / a.group;
+            const int64_t at = s.q0 + token;
+            const int h = head * a.group + x - token * a.group;
+            const float f = out_factor(l[nt][y], gv);
+            uint16_t* op = a.out + at * a.ld_ot + h * a.ld_oh + r * (D / 8);
+            if ((reinterpret_cast<uintptr_t>(op) & 15) == 0) {
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float mw = stat[(w * R + row) * 2];
-        const float f = mw == -INFINITY ? (stat[(w * R + row) * 2 + 1] == 0.0f ? 0.0f : 1.0f) : ex2(mw - top);
-        const float2 v = *reinterpret_cast<const float2*>(res + (w * R + row) * kPitch + d);
-        x0 += f * v.x;
-        x1 += f * v.y;
-        sum += f * stat[(w * R + row) * 2 + 1];
-      }
-      if (whole) {
-        store_row(row, d, x0, x1, top, sum);
-      } else {
-        *reinterpret_cast<float2*>(slot + row * D + d) = make_float2(x0, x1);
-        if (d == 0) *reinterpret_cast<float2*>(slot + R * D + 2 * row) = make_float2(top, sum);
-      }
-    }
-    if (!whole) {
-      // The last of the segment's CTAs to arrive joins the parts, in the order of their tokens.
-      __threadfence();
-      __syncthreads();
-      if (tid == 0) s_last = atomicAdd(a.counters + p_first, 1u) == uint32_t(p_last - p_first) ? 1 : 0;
-      __syncthreads();
-      if (s_last) {
-        __threadfence();
-        auto part = [&](int p) { return a.partials + (2 * int64_t(p) + (p == p_first ? 1 : 0)) * kSlot; };
-        for (int i = tid; i < rows * (D / 2); i += kAttnRowsThreads) {
-          const int row = i / (D / 2), d = 2 * (i % (D / 2));
-          float top = -INFINITY, x0 = 0.0f, x1 = 0.0f, sum = 0.0f;
-          for (int p = p_first; p <= p_last; ++p) {
-            const float2 st = __ldcg(reinterpret_cast<const float2*>(part(p) + R * D + 2 * row));
-            const float2 v = __ldcg(reinterpret_cast<const float2*>(part(p) + row * D + d));
-            const float up = fmaxf(top, st.x);
-            const float f0 = top == up ? 1.0f : ex2(top - up);
-            const float f1 = st.x == up ? 1.0f : ex2(st.x - up);
-            x0 = x0 * f0 + v.x * f1;
-            x1 = x1 * f0 + v.y * f1;
-            sum = sum * f0 + st.y * f1;
-            top = up;
+              for (int mt = 0; mt < D / 16; mt += 4) {
+                uint4 w;
+                w.x = pack_bf16x2(o[mt][nt][y] * f, o[mt][nt][y + 2] * f);
+                w.y = pack_bf16x2(o[mt + 1][nt][y] * f, o[mt + 1][nt][y + 2] * f);
+                w.z = pack_bf16x2(o[mt + 2][nt][y] * f, o[mt + 2][nt][y + 2] * f);
+                w.w = pack_bf16x2(o[mt + 3][nt][y] * f, o[mt + 3][nt][y + 2] * f);
+                *reinterpret_cast<uint4*>(op + 2 * mt) = w;
+              }
+            } else {
+#pragma unroll
+              for (int mt = 0; mt < D / 16; ++mt) store_pair(op + 2 * mt, o[mt][nt][y] * f, o[mt][nt][y + 2] * f);
+            }
+            if (a.lse != nullptr && r == 0) a.lse[at * a.ld_lse + h] = lse_of(m[nt][y], l[nt][y]);
           }
-          store_row(row, d, x0, x1, top, sum);
-        }
-        if (tid == 0) a.counters[p_first] = 0;
+      } else {
+        // A part: of a segment that began earlier, or of one that begins here.
+        const bool begins = seg0 >= u0;
+        float* slot = slot_of<D, R>(a, 2 * int64_t(part) + (begins ? 1 : 0));
+        if (begins) cut = {1, s.q0, tile * R, rows, head, owner_of(seg0 + units - 1), 0, 0};
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const int row = nt * 8 + 2 * j + y;
+            if (row >= rows) continue;
+            float* rp = slot + row * D + r * (D / 8);
+#pragma unroll
+            for (int mt = 0; mt < D / 16; mt += 2)
+              *reinterpret_cast<float4*>(rp + 2 * mt) =
+                  make_float4(o[mt][nt][y], o[mt][nt][y + 2], o[mt + 1][nt][y], o[mt + 1][nt][y + 2]);
+            if (r == 0) *reinterpret_cast<float2*>(slot + R * D + 2 * row) = make_float2(m[nt][y], l[nt][y]);
+          }
       }
+      u = seg0 + ub;
+    } else {
+      // The four warps' quarters of the chunk, through shared memory (over the rings).
+      float* res = reinterpret_cast<float*>(smem);  // [kWarps][R][kPitch]
+      float* stat = res + kWarps * R * kPitch;      // [kWarps][R][2]
+      __syncthreads();
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const int row = nt * 8 + 2 * j + y;
+          float* rp = res + (warp * R + row) * kPitch + r * (D / 8);
+#pragma unroll
+          for (int mt = 0; mt < D / 16; ++mt)
+            *reinterpret_cast<float2*>(rp + 2 * mt) = make_float2(o[mt][nt][y], o[mt][nt][y + 2]);
+          if (r == 0) *reinterpret_cast<float2*>(stat + (warp * R + row) * 2) = make_float2(m[nt][y], l[nt][y]);
+        }
+      __syncthreads();
+      float* slot = slot_of<D, R>(a, part);
+      for (int i = tid; i < rows * (D / 2); i += kAttnRowsThreads) {
+        const int row = i / (D / 2), d = 2 * (i % (D / 2));
+        float top = kLowest;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, stat[(w * R + row) * 2]);
+        float x0 = 0.0f, x1 = 0.0f, sum = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const float f = ex2(stat[(w * R + row) * 2] - top);
+          const float2 v = *reinterpret_cast<const float2*>(res + (w * R + row) * kPitch + d);
+          x0 += f * v.x;
+          x1 += f * v.y;
+          sum += f * stat[(w * R + row) * 2 + 1];
+        }
+        if (units == 1) {
+          const int x = tile * R + row, token = x / a.group;
+          const int64_t at = s.q0 + token;
+          const int h = head * a.group + x - token * a.group;
+          const float f = out_factor(sum, gv);
+          store_pair(a.out + at * a.ld_ot + h * a.ld_oh + d, x0 * f, x1 * f);
+          if (a.lse != nullptr && d == 0) a.lse[at * a.ld_lse + h] = lse_of(top, sum);
+        } else {
+          *reinterpret_cast<float2*>(slot + row * D + d) = make_float2(x0, x1);
+          if (d == 0) *reinterpret_cast<float2*>(slot + R * D + 2 * row) = make_float2(top, sum);
+        }
+      }
+      if (units > 1) {
+        __threadfence();
+        __syncthreads();
+        if (tid == 0) s_last = atomicAdd(counters_of(a) + seg0, 1u) == uint32_t(units - 1) ? 1 : 0;
+        __syncthreads();
+        if (s_last) {
+          __threadfence();
+          cut = {1, s.q0, tile * R, rows, head, 0, 0, 0};
+          reinterpret_cast<Join<D, R, kAttnRowsThreads>*>(smem)->run(
+              a, units, [&](int p) { return slot_of<D, R>(a, seg0 + p); }, cut, gv);
+          if (tid == 0) counters_of(a)[seg0] = 0;
+        }
+      }
+      return;
     }
-    __syncthreads();  // shared memory is free for the next segment
-    u = seg0 + ub;
   }
+  if (WALK && part < parts && lane == 0) cuts_of(a)[part] = cut;
+}
+
+// Joins the parts of a segment whose first part is blockIdx.x, if there is one.
+template <int D, int R>
+__global__ void __launch_bounds__(kAttnJoinThreads) rows_join_kernel(const AttnArgs a) {
+  __shared__ Join<D, R, kAttnJoinThreads> join;
+  const int first = int(blockIdx.x);
+  griddep_wait();
+  griddep_launch_dependents();
+  const int parts = __ldcg(parts_of(a));
+  const int4 c0 = __ldcg(reinterpret_cast<const int4*>(cuts_of(a) + first)), c1 = __ldcg(reinterpret_cast<const int4*>(cuts_of(a) + first) + 1);
+  if (first >= parts || !c0.x) return;
+  const Cut cut = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, 0, 0};
+  join.run(a, cut.last - first + 1, [&](int p) { return slot_of<D, R>(a, 2 * int64_t(first + p) + (p == 0 ? 1 : 0)); }, cut,
+           __ldg(a.v_scale));
 }
 
 }  // namespace
 
-const void* attn_rows_kernel(int d, int n_tiles) {
-#define NQ_ROWS(D, NT) \
-  if (d == D && n_tiles == NT) return reinterpret_cast<const void*>(&rows_kernel<D, NT>);
-  NQ_ROWS(64, 1) NQ_ROWS(64, 2) NQ_ROWS(128, 1) NQ_ROWS(128, 2) NQ_ROWS(256, 1) NQ_ROWS(256, 2)
+AttnRows attn_rows(int d, int n_tiles, bool walk) {
+#define NQ_ROWS(D, NT)                                                                                  \
+  if (d == D && n_tiles == NT) {                                                                        \
+    const size_t merge = merge_bytes(D, 8 * NT), join = sizeof(Join<D, 8 * NT, kAttnRowsThreads>);      \
+    const size_t need = walk ? 0 : (merge > join ? merge : join);                                       \
+    return {walk ? reinterpret_cast<const void*>(&rows_kernel<D, NT, true>)                             \
+                 : reinterpret_cast<const void*>(&rows_kernel<D, NT, false>),                           \
+            reinterpret_cast<const void*>(&rows_join_kernel<D, 8 * NT>), need > ring_bytes(D) ? need : ring_bytes(D)}; \
+  }
+  NQ_ROWS(64, 1) NQ_ROWS(64, 2) NQ_ROWS(64, 4) NQ_ROWS(128, 1) NQ_ROWS(128, 2) NQ_ROWS(256, 1) NQ_ROWS(256, 2)
 #undef NQ_ROWS
-  return nullptr;
-}
-
-size_t attn_rows_smem(int d, int n_tiles) {
-  const size_t m = merge_bytes(d, 8 * n_tiles);
-  return m > ring_bytes(d) ? m : ring_bytes(d);
+  return {nullptr, nullptr, 0};
 }
 
 }  // namespace nq

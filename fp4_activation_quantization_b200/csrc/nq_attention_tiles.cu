@@ -161,6 +161,8 @@ struct Item {
   int index, split;   // number of the item among tiles and heads, of the split
 };
 
+__device__ __forceinline__ float* partials_of(const AttnArgs& a) { return reinterpret_cast<float*>(a.workspace + kAttnHeader); }
+
 template <int R>
 __device__ __forceinline__ int64_t tile_start(const AttnArgs& a, int b, int c0) {
   return int64_t(c0) * a.group / R + b;
@@ -532,7 +534,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
     const float l = (l2[0].x + l2[0].y) + (l2[1].x + l2[1].y);
     const int64_t at = it.q0 + token;
     float* part = nullptr;
-    if (a.splits > 1) part = a.partials + (int64_t(it.index) * a.splits + it.split) * (C::kRows * (D + 2)) + row * D;
+    if (a.splits > 1) part = partials_of(a) + (int64_t(it.index) * a.splits + it.split) * (C::kRows * (D + 2)) + row * D;
     const float f = l > 0.0f || l != l ? __ldg(a.v_scale) / l : 0.0f;
     if (ok) {
 #pragma unroll 1
@@ -809,7 +811,7 @@ __global__ void __launch_bounds__(256) join_kernel(const AttnArgs a) {
   const int row = part * 8 + int(threadIdx.x >> 5), lane = int(threadIdx.x) & 31;
   if (row >= it.rows) return;
   const int x = it.row0 + row, token = x / a.group, head = it.head * a.group + x - token * a.group;
-  const float* base = a.partials + int64_t(it.index) * a.splits * kSlot;
+  const float* base = partials_of(a) + int64_t(it.index) * a.splits * kSlot;
   float top = -INFINITY, l = 0.0f;
   float o[D / 32];
 #pragma unroll

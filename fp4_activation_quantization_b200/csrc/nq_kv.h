@@ -70,20 +70,21 @@ struct AttnArgs {
   int64_t ld_ot, ld_oh;
   float* lse;  // [T, ld_lse] or null
   int64_t ld_lse;
-  uint32_t* counters;  // arrivals per split tile, zero between calls
-  float* partials;
+  uint8_t* workspace;  // parts of rows whose keys were split
   int32_t T, B, heads, group;  // group: query heads per kv head
   int32_t window;              // 0: none
   int32_t causal;
   float scale_log2;  // softmax scale * log2(e)
-  int32_t max_splits;  // rows kernel: parts of a segment on average, at most
   int32_t tiles;       // tiles kernel: row tiles counted over the batch
   int32_t splits;      // tiles kernel: parts of an item's keys
   uint32_t* err;
 };
 
-// Counters at the head of the attention workspace; partial results follow.
-constexpr int kAttnCounters = 16384;
+// The head of the attention workspace: counters, zero between calls, then what
+// describes the parts; their values follow.
+constexpr int kAttnCounterBytes = 1 << 14;
+constexpr int kAttnHeader = 1 << 19;
+constexpr int kAttnMaxParts = (kAttnHeader - kAttnCounterBytes - 64) / 32;
 
 // Kernels (nullptr: not built).
 const void* kv_plan_kernel();
@@ -92,9 +93,13 @@ const void* kv_gather_kernel(int d, bool vec);
 constexpr int kKvPlanThreads = 512;
 constexpr int kKvCopyThreads = 256;
 
-constexpr int kAttnRowsThreads = 128;
-const void* attn_rows_kernel(int d, int n_tiles);       // n_tiles: 8-row tiles per warp, 1 or 2
-size_t attn_rows_smem(int d, int n_tiles);
+constexpr int kAttnRowsThreads = 128, kAttnJoinThreads = 256;
+struct AttnRows {
+  const void* kernel;
+  const void* join;  // walk: a CTA per part, after it
+  size_t smem;
+};
+AttnRows attn_rows(int d, int n_tiles, bool walk);  // n_tiles: 8-row tiles of a warp
 
 constexpr int kAttnTilesThreads = 512;
 struct AttnTiles {

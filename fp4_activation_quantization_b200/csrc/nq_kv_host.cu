@@ -142,10 +142,10 @@ nq_status nq_kv_plan(const int32_t* cached_lens, const int32_t* new_lens, int32_
   a.err = nq::host::error_word();
   if (a.err == nullptr) return error(NQ_ERR_CUDA, "%s: no CUDA device", fn);
   const void* k = nq::kv_plan_kernel();
-  const size_t smem = size_t(2 * (B + 1)) * sizeof(int32_t);
+  const size_t smem = size_t(3 * B + 2) * sizeof(int32_t);
   if (!nq::host::allow_smem(k, smem)) return error(NQ_ERR_UNSUPPORTED, "%s: %zu bytes of shared memory not available", fn, smem);
-  // Every CTA repeats the scan, so no more of them than keep four tokens a thread.
-  int64_t grid = (T + 4 * nq::kKvPlanThreads - 1) / (4 * nq::kKvPlanThreads);
+  // Every CTA repeats the scan; one token a thread as far as the SMs go (B = 2048, T = 95647: 8.0 us with four).
+  int64_t grid = (T + nq::kKvPlanThreads - 1) / nq::kKvPlanThreads;
   grid = grid < 1 ? 1 : (grid > 148 ? 148 : grid);
   if (free_head_out == free_head) grid = 1;  // every CTA reads the head: only a lone one may overwrite it
   void* args[] = {&a};
@@ -212,8 +212,7 @@ nq_status nq_attention_nvfp4_kv(const void* q, int64_t ld_q_token, int64_t ld_q_
   a.ld_ot = ld_out_token, a.ld_oh = ld_out_head;
   a.lse = lse;
   a.ld_lse = ld_lse;
-  a.counters = static_cast<uint32_t*>(workspace);
-  a.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + sizeof(uint32_t) * nq::kAttnCounters);
+  a.workspace = static_cast<uint8_t*>(workspace);
   a.T = int32_t(T);
   a.B = int32_t(B);
   a.heads = heads;
@@ -221,20 +220,18 @@ nq_status nq_attention_nvfp4_kv(const void* q, int64_t ld_q_token, int64_t ld_q_
   a.window = window;
   a.causal = (flags & NQ_FLAG_NONCAUSAL) ? 0 : 1;
   a.scale_log2 = softmax_scale * 1.44269504088896340736f;
-  a.max_splits = 64;
   a.err = nq::host::error_word();
   if (a.err == nullptr) return error(NQ_ERR_CUDA, "%s: no CUDA device", fn);
 
   const int64_t rows = (T * a.group + B - 1) / B;  // of an average request and kv head
-  if (rows > 16) {
+  if (rows > (d == 64 ? 64 : 32)) {
     const nq::AttnTiles k = nq::attn_tiles(d);
     if (!nq::host::allow_smem(k.kernel, k.smem))
       return error(NQ_ERR_UNSUPPORTED, "%s: %zu bytes of shared memory not available", fn, k.smem);
     const int64_t tiles = T * a.group / k.rows + B, items = tiles * kv_heads;
     const int64_t sms = nq::host::resident_ctas(k.kernel, nq::kAttnTilesThreads, k.smem);
     if (sms <= 0) return error(NQ_ERR_CUDA, "%s: no CUDA device", fn);
-    const int64_t room = (workspace_bytes - int64_t(sizeof(uint32_t)) * nq::kAttnCounters) /
-                         (int64_t(k.rows) * (d + 2) * int64_t(sizeof(float)));
+    const int64_t room = (workspace_bytes - nq::kAttnHeader) / (int64_t(k.rows) * (d + 2) * int64_t(sizeof(float)));
     int64_t splits = (sms < room ? sms : room) / items;
     const int64_t blocks = (int64_t(table_width) * page_size + 511) / 512;  // at least four blocks of keys each
     splits = splits < blocks ? splits : blocks;
@@ -251,23 +248,41 @@ nq_status nq_attention_nvfp4_kv(const void* q, int64_t ld_q_token, int64_t ld_q_
                            static_cast<cudaStream_t>(stream));
     return s;
   }
-  const int n_tiles = rows <= 8 ? 1 : 2;
-  const void* k = nq::attn_rows_kernel(d, n_tiles);
-  const size_t smem = nq::attn_rows_smem(d, n_tiles);
-  if (!nq::host::allow_smem(k, smem)) return error(NQ_ERR_UNSUPPORTED, "%s: %zu bytes of shared memory not available", fn, smem);
-  int64_t grid = nq::host::resident_ctas(k, nq::kAttnRowsThreads, smem);
-  if (grid <= 0) return error(NQ_ERR_CUDA, "%s: no CUDA device", fn);
-  // Not more than there can be units of 64 tokens, nor than the workspace has room for (two parts a CTA).
+  const int n_tiles = rows <= 8 ? 1 : (rows <= 16 || d > 64 ? 2 : 4);
+  // Fewer segments (request, row tile, kv head) than half the CTAs that the GPU holds: a chunk a CTA and one
+  // launch; else a share a warp and a second launch.
+  constexpr int kWarps = nq::kAttnRowsThreads / 32;
   const int64_t segments = (T * a.group / (8 * n_tiles) + B) * kv_heads;
-  const int64_t units = (int64_t(table_width) * page_size + 63) / 64;
-  if (units < 4096 && segments < 4096 && segments * (units < 1 ? 1 : units) < grid) grid = segments * (units < 1 ? 1 : units);
-  const int64_t room = (workspace_bytes - int64_t(sizeof(uint32_t)) * nq::kAttnCounters) /
-                       (2 * int64_t(8 * n_tiles) * (d + 2) * int64_t(sizeof(float)));
-  grid = grid < room ? grid : room;
-  grid = grid < nq::kAttnCounters ? grid : nq::kAttnCounters;
+  const int64_t slot = int64_t(8 * n_tiles) * (d + 2) * int64_t(sizeof(float));
+  const int64_t atoms = (int64_t(table_width) * page_size + 15) / 16;
+  nq::AttnRows k = nq::attn_rows(d, n_tiles, false);
+  if (!nq::host::allow_smem(k.kernel, k.smem))
+    return error(NQ_ERR_UNSUPPORTED, "%s: %zu bytes of shared memory not available", fn, k.smem);
+  int64_t grid = nq::host::resident_ctas(k.kernel, nq::kAttnRowsThreads, k.smem);
+  if (grid <= 0) return error(NQ_ERR_CUDA, "%s: no CUDA device", fn);
   void* args[] = {&a};
-  return nq::host::launch(fn, k, unsigned(grid), nq::kAttnRowsThreads, smem, args, (flags & NQ_FLAG_PDL) != 0,
-                          static_cast<cudaStream_t>(stream));
+  if (segments <= grid / 2) {
+    const int64_t room = (workspace_bytes - nq::kAttnHeader) / slot, counters = nq::kAttnCounterBytes / 4;
+    grid = grid < room ? grid : room;
+    grid = grid < counters ? grid : counters;
+    if (segments * (atoms / 32 + 1) < grid) grid = segments * (atoms / 32 + 1);
+    return nq::host::launch(fn, k.kernel, unsigned(grid), nq::kAttnRowsThreads, k.smem, args, (flags & NQ_FLAG_PDL) != 0,
+                            static_cast<cudaStream_t>(stream));
+  }
+  k = nq::attn_rows(d, n_tiles, true);
+  if (!nq::host::allow_smem(k.kernel, k.smem))
+    return error(NQ_ERR_UNSUPPORTED, "%s: %zu bytes of shared memory not available", fn, k.smem);
+  grid = nq::host::resident_ctas(k.kernel, nq::kAttnRowsThreads, k.smem);
+  if (grid <= 0) return error(NQ_ERR_CUDA, "%s: no CUDA device", fn);
+  int64_t room = (workspace_bytes - nq::kAttnHeader) / (2 * slot);
+  room = room < nq::kAttnMaxParts ? room : nq::kAttnMaxParts;
+  grid = grid < room / kWarps ? grid : room / kWarps;
+  nq_status s = nq::host::launch(fn, k.kernel, unsigned(grid), nq::kAttnRowsThreads, k.smem, args,
+                                 (flags & NQ_FLAG_PDL) != 0, static_cast<cudaStream_t>(stream));
+  if (s == NQ_OK)  // may start while the first launch ends; it waits for its results
+    s = nq::host::launch(fn, k.join, unsigned(grid * kWarps), nq::kAttnJoinThreads, 0, args, true,
+                         static_cast<cudaStream_t>(stream));
+  return s;
 }
 
 }  // extern "C"

@@ -52,6 +52,7 @@ __global__ void __launch_bounds__(kKvPlanThreads) plan_kernel(const KvPlanArgs a
   extern __shared__ int32_t smem[];
   int32_t* first_token = smem;           // [B + 1]
   int32_t* first_page = smem + a.B + 1;  // [B + 1]
+  int32_t* cached = first_page + a.B + 1;  // [B]
   __shared__ uint64_t warp_sum[kKvPlanThreads / 32];
   constexpr int kItems = 4;
   const int tid = int(threadIdx.x), lane = tid & 31, warp = tid >> 5;
@@ -70,6 +71,7 @@ __global__ void __launch_bounds__(kKvPlanThreads) plan_kernel(const KvPlanArgs a
       if (b < a.B) {
         const Request r = request_of(a, b, &bad);
         item[i] = (uint64_t(uint32_t(r.tokens)) << 32) | uint32_t(r.pages);
+        cached[b] = r.cached;
       }
     }
 #pragma unroll
@@ -116,6 +118,9 @@ __global__ void __launch_bounds__(kKvPlanThreads) plan_kernel(const KvPlanArgs a
     const int64_t at = head + i;
     return at >= 0 && at < a.n_free ? a.free_pages[at] : -1;
   };
+  auto held = [&](int b) {  // pages that request b holds
+    return int(min((int64_t(cached[b]) + (1 << a.log_page) - 1) >> a.log_page, int64_t(a.width)));
+  };
   for (int b = me; b <= a.B; b += step) {
     a.cu_q[b] = first_token[b];
     if (b < a.B) {
@@ -128,9 +133,7 @@ __global__ void __launch_bounds__(kKvPlanThreads) plan_kernel(const KvPlanArgs a
   }
   for (int f = me; f < pages; f += step) {
     const int b = last_not_above(first_page, a.B, f);
-    bool unused = false;
-    const Request r = request_of(a, b, &unused);
-    a.table[b * a.ld_table + r.have + (f - first_page[b])] = fresh(f);
+    a.table[b * a.ld_table + held(b) + (f - first_page[b])] = fresh(f);
   }
   const int32_t mask = (1 << a.log_page) - 1;
   for (int t = me; t < a.T; t += step) {
@@ -138,13 +141,12 @@ __global__ void __launch_bounds__(kKvPlanThreads) plan_kernel(const KvPlanArgs a
     int64_t slot = -1;
     if (t < first_token[a.B]) {
       const int b = last_not_above(first_token, a.B, t);
-      bool unused = false;
-      const Request r = request_of(a, b, &unused);
-      const int64_t at = int64_t(r.cached) + (t - first_token[b]);
+      const int64_t at = int64_t(cached[b]) + (t - first_token[b]);
       const int64_t p = at >> a.log_page;
       pos = int32_t(min(at, int64_t(0x7fffffff)));
       if (p < a.width) {
-        const int32_t page = p < r.have ? a.table[b * a.ld_table + p] : fresh(int64_t(first_page[b]) + (p - r.have));
+        const int have = held(b);
+        const int32_t page = p < have ? a.table[b * a.ld_table + p] : fresh(int64_t(first_page[b]) + (p - have));
         if (page >= 0) slot = (int64_t(page) << a.log_page) + (at & mask);
       }
     }

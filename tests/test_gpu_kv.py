@@ -307,12 +307,9 @@ def test_prompt_rows_beyond_the_keys(nq, D):
 @pytest.mark.parametrize("D,heads,kv_heads", [(64, 8, 1), (128, 4, 1), (128, 16, 8), (256, 2, 1)])
 def test_one_long_request_is_split_over_the_gpu(nq, D, heads, kv_heads):
     ws = torch.zeros(nq.ATTENTION_WORKSPACE_BYTES, dtype=torch.uint8, device="cuda")
-    s = make(nq, [1], [40001], heads, kv_heads, D, 128, seed=2)
-    check(nq, s, workspace=ws)
-    assert not ws[:65536].any()  # ready for the next call
-    s = make(nq, [70], [9000], heads, kv_heads, D, 128, seed=2)
-    check(nq, s, workspace=ws)
-    assert not ws[:65536].any()
+    # one workspace for calls that split their keys in different ways, one after another
+    for n, t in (([1], [40001]), ([70], [9000]), ([1, 1], [700, 33]), ([1] * 700, [90] * 699 + [9000]), ([1], [40001])):
+        check(nq, make(nq, n, t, heads, kv_heads, D, 128, seed=2), workspace=ws)
 
 
 @pytest.mark.parametrize("n,t", [([1] * 5, [3000] * 5), ([200, 90], [1500, 900])])
