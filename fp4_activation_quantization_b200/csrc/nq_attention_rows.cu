@@ -42,14 +42,14 @@ namespace nq {
 
 namespace {
 
-constexpr int kWarps = kAttnRowsThreads / 32;
+constexpr int kWalkWarps = 4, kChunkWarps = 8;
 constexpr float kRaise = 8.0f;      // log2 by which a score may exceed the running maximum
 constexpr float kLowest = -3.0e38f; // the maximum of no scores: below every finite one, and 0 * 2^(kLowest - kLowest) is 0
 
 constexpr int stages_of(int d) { return d == 256 ? 3 : 4; }
-constexpr size_t ring_bytes(int d) { return size_t(kWarps) * stages_of(d) * 18 * d; }
+constexpr size_t ring_bytes(int d, int warps) { return size_t(warps) * stages_of(d) * 18 * d; }
 constexpr int row_pitch(int d) { return d + 4; }  // floats between rows of a warp's result in shared memory
-constexpr size_t merge_bytes(int d, int rows) { return size_t(kWarps) * rows * (row_pitch(d) + 2) * 4; }
+constexpr size_t merge_bytes(int d, int rows) { return size_t(kChunkWarps) * rows * (row_pitch(d) + 2) * 4; }
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -93,17 +93,21 @@ struct Span {
   int first;              // first key any row sees, rounded down to an atom
   int tiles, units;       // row tiles; atoms of keys per tile and kv head
 };
+// A quotient that mostly fits 32 bits (a 64-bit division is 100 instructions).
+__device__ __forceinline__ int64_t quotient(int64_t x, int64_t d) {
+  return (uint64_t(x | d) >> 32) == 0 ? int64_t(uint32_t(x) / uint32_t(d)) : x / d;
+}
 template <int R>
 __device__ __forceinline__ Span span_of(const AttnArgs& a, int b) {
   Span s;
-  const int64_t room = int64_t(a.width) << a.cache.log_page;
-  const int c0 = min(max(a.cu_q[b], 0), a.T), c1 = min(max(a.cu_q[b + 1], c0), a.T);
+  const int room = a.width << a.cache.log_page;  // at most 2^30, as the window; rows stay below 2^30 too
+  const int c0 = min(max(__ldg(a.cu_q + b), 0), a.T), c1 = min(max(__ldg(a.cu_q + b + 1), c0), a.T);
   s.q0 = c0;
   s.q_len = c1 - c0;
-  s.kv_len = int(min(int64_t(max(a.kv_lens[b], 0)), room));
+  s.kv_len = min(max(__ldg(a.kv_lens + b), 0), room);
   s.first = 0;
-  if (a.window > 0) s.first = int(max(int64_t(0), int64_t(s.kv_len) - s.q_len + 1 - a.window)) & ~15;
-  s.tiles = int((int64_t(s.q_len) * a.group + R - 1) / R);
+  if (a.window > 0) s.first = max(0, s.kv_len - s.q_len + 1 - a.window) & ~15;
+  s.tiles = (s.q_len * a.group + R - 1) / R;
   s.units = max(1, (s.kv_len - s.first + 15) >> 4);
   return s;
 }
@@ -233,8 +237,10 @@ struct Join {
 };
 
 template <int D, int NT, bool WALK>
-__global__ void __launch_bounds__(kAttnRowsThreads, D == 256 ? 2 : (NT == 1 ? 4 : (NT == 2 ? 3 : 2)))
+__global__ void __launch_bounds__((WALK ? kWalkWarps : kChunkWarps) * 32,
+                                  (D == 256 ? 2 : (NT == 1 ? 4 : (NT == 2 ? 3 : 2))) * kWalkWarps / (WALK ? kWalkWarps : kChunkWarps))
     rows_kernel(const AttnArgs a) {
+  constexpr int kWarps = WALK ? kWalkWarps : kChunkWarps, kThreads = kWarps * 32;
   constexpr int R = 8 * NT;  // rows of a tile: (token, head of the group), token-major
   constexpr int kStages = stages_of(D);
   constexpr int kN = KvAtom<D>::kN, kW = KvAtom<D>::kW;
@@ -252,7 +258,7 @@ __global__ void __launch_bounds__(kAttnRowsThreads, D == 256 ? 2 : (NT == 1 ? 4 
   griddep_launch_dependents();
 
   // ---- the axis: atoms of all requests (each thread counts a run of them)
-  const int per = (a.B + kAttnRowsThreads - 1) / kAttnRowsThreads;
+  const int per = (a.B + kThreads - 1) / kThreads;
   const int b_lo = min(a.B, tid * per), b_hi = min(a.B, b_lo + per);
   // Sum of `mine` over the CTA's threads, and over those before this one.
   auto scan = [&](int64_t mine, int64_t* before) {
@@ -289,8 +295,8 @@ __global__ void __launch_bounds__(kAttnRowsThreads, D == 256 ? 2 : (NT == 1 ? 4 
   auto part_of_warp = [&](int w) {
     return parts == int(gridDim.x) * kWarps ? int(blockIdx.x) * kWarps + w : w * int(gridDim.x) + int(blockIdx.x);
   };
-  auto start_of = [&](int64_t p) { return total * p / parts; };
-  auto owner_of = [&](int64_t u) { return int(((u + 1) * parts - 1) / total); };
+  auto start_of = [&](int64_t p) { return quotient(total * p, parts); };
+  auto owner_of = [&](int64_t u) { return int(quotient((u + 1) * parts - 1, total)); };
   if constexpr (WALK) {
     parts = int(min(int64_t(gridDim.x) * kWarps, (total + 1) >> 1));
     if (blockIdx.x == 0 && tid == 0) *parts_of(a) = parts;
@@ -354,10 +360,18 @@ __global__ void __launch_bounds__(kAttnRowsThreads, D == 256 ? 2 : (NT == 1 ? 4 
     }
     // ---- segment (request b, row tile, kv head): atoms [ua, ub) of it are this warp's
     const int units = units_of(s);
-    const int64_t seg = (u - base) / units;
-    const int64_t seg0 = base + seg * units;
-    const int tile = int(seg / heads), head = int(seg - int64_t(tile) * heads);
+    const int seg = int(quotient(u - base, units));
+    const int64_t seg0 = base + int64_t(seg) * units;
+    const int tile = seg / heads, head = seg - tile * heads;
     const int rows = min(R, s.q_len * a.group - tile * R);
+    // Row y of the tile is head g of token: one division here, then of numbers
+    // below group + R by a multiplication (exact: their product stays below 2^32).
+    const int token0 = tile * R / a.group, rest0 = tile * R - token0 * a.group;
+    auto token_of = [&](int y, int* g) {
+      const uint32_t x = uint32_t(rest0 + y), q = a.group == 1 ? x : __umulhi(x, a.group_magic);
+      *g = int(x) - int(q) * a.group;
+      return token0 + int(q);
+    };
     int ua, ub;
     if constexpr (WALK) {
       ua = int(u - seg0);
@@ -380,9 +394,10 @@ __global__ void __launch_bounds__(kAttnRowsThreads, D == 256 ? 2 : (NT == 1 ? 4 
         lo[nt][i] = 0;
         hi[nt][i] = 0;
         if (row < rows) {
-          const int64_t pos = int64_t(s.kv_len) - s.q_len + (tile * R + row) / a.group;
-          hi[nt][i] = a.causal ? int(min(int64_t(s.kv_len), max(int64_t(0), pos + 1))) : s.kv_len;
-          lo[nt][i] = a.window > 0 ? int(max(int64_t(0), pos + 1 - a.window)) : 0;
+          int g;
+          const int pos = s.kv_len - s.q_len + token_of(row, &g);
+          hi[nt][i] = a.causal ? min(s.kv_len, max(0, pos + 1)) : s.kv_len;
+          lo[nt][i] = a.window > 0 ? max(0, pos + 1 - a.window) : 0;
           lo_all = min(lo_all, lo[nt][i]);
           hi_all = max(hi_all, hi[nt][i]);
           lo_full = max(lo_full, lo[nt][i]);
@@ -446,7 +461,8 @@ __global__ void __launch_bounds__(kAttnRowsThreads, D == 256 ? 2 : (NT == 1 ? 4 
       uint4 raw[D / 32];
       float amax = 0.0f;
       if (row < rows) {
-        const int x = tile * R + row, token = x / a.group, g = x - token * a.group;
+        int g;
+        const int token = token_of(row, &g);
         const uint16_t* qp = a.q + int64_t(s.q0 + token) * a.ld_qt + int64_t(head * a.group + g) * a.ld_qh + j * (D / 4);
         if ((reinterpret_cast<uintptr_t>(qp) & 15) == 0) {
 #pragma unroll
@@ -705,9 +721,9 @@ __global__ void __launch_bounds__(kAttnRowsThreads, D == 256 ? 2 : (NT == 1 ? 4 
           for (int y = 0; y < 2; ++y) {
             const int row = nt * 8 + 2 * j + y;
             if (row >= rows) continue;
-            const int x = tile * R + row, token = x / a.group;
-            const int64_t at = s.q0 + token;
-            const int h = head * a.group + x - token * a.group;
+            int g;
+            const int64_t at = s.q0 + token_of(row, &g);
+            const int h = head * a.group + g;
             const float f = out_factor(l[nt][y], gv);
             uint16_t* op = a.out + at * a.ld_ot + h * a.ld_oh + r * (D / 8);
             if ((reinterpret_cast<uintptr_t>(op) & 15) == 0) {
@@ -764,7 +780,7 @@ __global__ void __launch_bounds__(kAttnRowsThreads, D == 256 ? 2 : (NT == 1 ? 4 
         }
       __syncthreads();
       float* slot = slot_of<D, R>(a, part);
-      for (int i = tid; i < rows * (D / 2); i += kAttnRowsThreads) {
+      for (int i = tid; i < rows * (D / 2); i += kThreads) {
         const int row = i / (D / 2), d = 2 * (i % (D / 2));
         float top = kLowest;
 #pragma unroll
@@ -779,9 +795,9 @@ __global__ void __launch_bounds__(kAttnRowsThreads, D == 256 ? 2 : (NT == 1 ? 4 
           sum += f * stat[(w * R + row) * 2 + 1];
         }
         if (units == 1) {
-          const int x = tile * R + row, token = x / a.group;
-          const int64_t at = s.q0 + token;
-          const int h = head * a.group + x - token * a.group;
+          int g;
+          const int64_t at = s.q0 + token_of(row, &g);
+          const int h = head * a.group + g;
           const float f = out_factor(sum, gv);
           store_pair(a.out + at * a.ld_ot + h * a.ld_oh + d, x0 * f, x1 * f);
           if (a.lse != nullptr && d == 0) a.lse[at * a.ld_lse + h] = lse_of(top, sum);
@@ -798,7 +814,7 @@ __global__ void __launch_bounds__(kAttnRowsThreads, D == 256 ? 2 : (NT == 1 ? 4 
         if (s_last) {
           __threadfence();
           cut = {1, s.q0, tile * R, rows, head, 0, 0, 0};
-          reinterpret_cast<Join<D, R, kAttnRowsThreads>*>(smem)->run(
+          reinterpret_cast<Join<D, R, kThreads>*>(smem)->run(
               a, units, [&](int p) { return slot_of<D, R>(a, seg0 + p); }, cut, gv);
           if (tid == 0) counters_of(a)[seg0] = 0;
         }
@@ -829,15 +845,16 @@ __global__ void __launch_bounds__(kAttnJoinThreads) rows_join_kernel(const AttnA
 AttnRows attn_rows(int d, int n_tiles, bool walk) {
 #define NQ_ROWS(D, NT)                                                                                  \
   if (d == D && n_tiles == NT) {                                                                        \
-    const size_t merge = merge_bytes(D, 8 * NT), join = sizeof(Join<D, 8 * NT, kAttnRowsThreads>);      \
+    const size_t merge = merge_bytes(D, 8 * NT), join = sizeof(Join<D, 8 * NT, kChunkWarps * 32>);      \
+    const size_t ring = ring_bytes(D, walk ? kWalkWarps : kChunkWarps);                                 \
     const size_t need = walk ? 0 : (merge > join ? merge : join);                                       \
     return {walk ? reinterpret_cast<const void*>(&rows_kernel<D, NT, true>)                             \
                  : reinterpret_cast<const void*>(&rows_kernel<D, NT, false>),                           \
-            reinterpret_cast<const void*>(&rows_join_kernel<D, 8 * NT>), need > ring_bytes(D) ? need : ring_bytes(D)}; \
+            reinterpret_cast<const void*>(&rows_join_kernel<D, 8 * NT>), need > ring ? need : ring, (walk ? kWalkWarps : kChunkWarps) * 32}; \
   }
   NQ_ROWS(64, 1) NQ_ROWS(64, 2) NQ_ROWS(64, 4) NQ_ROWS(128, 1) NQ_ROWS(128, 2) NQ_ROWS(256, 1) NQ_ROWS(256, 2)
 #undef NQ_ROWS
-  return {nullptr, nullptr, 0};
+  return {nullptr, nullptr, 0, 0};
 }
 
 }  // namespace nq

@@ -72,6 +72,7 @@ struct AttnArgs {
   int64_t ld_lse;
   uint8_t* workspace;  // parts of rows whose keys were split
   int32_t T, B, heads, group;  // group: query heads per kv head
+  uint32_t group_magic;        // ceil(2^32 / group)
   int32_t window;              // 0: none
   int32_t causal;
   float scale_log2;  // softmax scale * log2(e)
@@ -93,11 +94,12 @@ const void* kv_gather_kernel(int d, bool vec);
 constexpr int kKvPlanThreads = 512;
 constexpr int kKvCopyThreads = 256;
 
-constexpr int kAttnRowsThreads = 128, kAttnJoinThreads = 256;
+constexpr int kAttnJoinThreads = 256;
 struct AttnRows {
   const void* kernel;
   const void* join;  // walk: a CTA per part, after it
   size_t smem;
+  int threads;
 };
 AttnRows attn_rows(int d, int n_tiles, bool walk);  // n_tiles: 8-row tiles of a warp
 

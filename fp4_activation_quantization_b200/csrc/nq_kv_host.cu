@@ -184,7 +184,8 @@ nq_status nq_attention_nvfp4_kv(const void* q, int64_t ld_q_token, int64_t ld_q_
   NQ_REQUIRE(heads >= kv_heads && heads % kv_heads == 0, "%s: heads = %d is not a multiple of kv_heads = %d", fn, heads,
              kv_heads);
   NQ_REQUIRE(T >= 0 && B >= 0, "%s: negative size", fn);
-  if (T > kInt32Max / heads || B > (1 << 24)) return error(NQ_ERR_UNSUPPORTED, "%s: T or B too large", fn);
+  if (heads / kv_heads > 1024) return error(NQ_ERR_UNSUPPORTED, "%s: more than 1024 query heads per kv head", fn);
+  if (T > (1 << 30) / heads || B > (1 << 24)) return error(NQ_ERR_UNSUPPORTED, "%s: T or B too large", fn);
   NQ_REQUIRE(std::isfinite(softmax_scale), "%s: softmax_scale must be finite", fn);
   NQ_REQUIRE(window >= 0, "%s: window = %d < 0", fn, window);
   NQ_REQUIRE(table_width >= 0 && ld_table >= table_width, "%s: ld_table must be >= table_width", fn);
@@ -217,7 +218,8 @@ nq_status nq_attention_nvfp4_kv(const void* q, int64_t ld_q_token, int64_t ld_q_
   a.B = int32_t(B);
   a.heads = heads;
   a.group = heads / kv_heads;
-  a.window = window;
+  a.window = window < (1 << 30) ? window : 1 << 30;  // no key is further away
+  a.group_magic = uint32_t(((uint64_t(1) << 32) + a.group - 1) / a.group);
   a.causal = (flags & NQ_FLAG_NONCAUSAL) ? 0 : 1;
   a.scale_log2 = softmax_scale * 1.44269504088896340736f;
   a.err = nq::host::error_word();
@@ -251,14 +253,13 @@ nq_status nq_attention_nvfp4_kv(const void* q, int64_t ld_q_token, int64_t ld_q_
   const int n_tiles = rows <= 8 ? 1 : (rows <= 16 || d > 64 ? 2 : 4);
   // Fewer segments (request, row tile, kv head) than half the CTAs that the GPU holds: a chunk a CTA and one
   // launch; else a share a warp and a second launch.
-  constexpr int kWarps = nq::kAttnRowsThreads / 32;
   const int64_t segments = (T * a.group / (8 * n_tiles) + B) * kv_heads;
   const int64_t slot = int64_t(8 * n_tiles) * (d + 2) * int64_t(sizeof(float));
   const int64_t atoms = (int64_t(table_width) * page_size + 15) / 16;
   nq::AttnRows k = nq::attn_rows(d, n_tiles, false);
   if (!nq::host::allow_smem(k.kernel, k.smem))
     return error(NQ_ERR_UNSUPPORTED, "%s: %zu bytes of shared memory not available", fn, k.smem);
-  int64_t grid = nq::host::resident_ctas(k.kernel, nq::kAttnRowsThreads, k.smem);
+  int64_t grid = nq::host::resident_ctas(k.kernel, k.threads, k.smem);
   if (grid <= 0) return error(NQ_ERR_CUDA, "%s: no CUDA device", fn);
   void* args[] = {&a};
   if (segments <= grid / 2) {
@@ -266,21 +267,22 @@ nq_status nq_attention_nvfp4_kv(const void* q, int64_t ld_q_token, int64_t ld_q_
     grid = grid < room ? grid : room;
     grid = grid < counters ? grid : counters;
     if (segments * (atoms / 32 + 1) < grid) grid = segments * (atoms / 32 + 1);
-    return nq::host::launch(fn, k.kernel, unsigned(grid), nq::kAttnRowsThreads, k.smem, args, (flags & NQ_FLAG_PDL) != 0,
+    return nq::host::launch(fn, k.kernel, unsigned(grid), k.threads, k.smem, args, (flags & NQ_FLAG_PDL) != 0,
                             static_cast<cudaStream_t>(stream));
   }
   k = nq::attn_rows(d, n_tiles, true);
   if (!nq::host::allow_smem(k.kernel, k.smem))
     return error(NQ_ERR_UNSUPPORTED, "%s: %zu bytes of shared memory not available", fn, k.smem);
-  grid = nq::host::resident_ctas(k.kernel, nq::kAttnRowsThreads, k.smem);
+  grid = nq::host::resident_ctas(k.kernel, k.threads, k.smem);
+  const int warps = k.threads / 32;
   if (grid <= 0) return error(NQ_ERR_CUDA, "%s: no CUDA device", fn);
   int64_t room = (workspace_bytes - nq::kAttnHeader) / (2 * slot);
   room = room < nq::kAttnMaxParts ? room : nq::kAttnMaxParts;
-  grid = grid < room / kWarps ? grid : room / kWarps;
-  nq_status s = nq::host::launch(fn, k.kernel, unsigned(grid), nq::kAttnRowsThreads, k.smem, args,
+  grid = grid < room / warps ? grid : room / warps;
+  nq_status s = nq::host::launch(fn, k.kernel, unsigned(grid), k.threads, k.smem, args,
                                  (flags & NQ_FLAG_PDL) != 0, static_cast<cudaStream_t>(stream));
   if (s == NQ_OK)  // may start while the first launch ends; it waits for its results
-    s = nq::host::launch(fn, k.join, unsigned(grid * kWarps), nq::kAttnJoinThreads, 0, args, true,
+    s = nq::host::launch(fn, k.join, unsigned(grid * warps), nq::kAttnJoinThreads, 0, args, true,
                          static_cast<cudaStream_t>(stream));
   return s;
 }

@@ -25,6 +25,7 @@ def test_attention_refusals(nq):
     assert attend(nq, page=8) == UNS and attend(nq, page=24) == UNS and attend(nq, page=256) == UNS
     assert attend(nq, heads=7) == INV and attend(nq, heads=1) == INV
     assert attend(nq, kv_heads=0) == INV
+    assert attend(nq, heads=1025, kv_heads=1, ld_lse=1025) == UNS
     assert attend(nq, q=None) == INV and attend(nq, cache=None) == INV and attend(nq, table=None) == INV
     assert attend(nq, ws=None) == INV and attend(nq, ws=FAKE + 8) == INV
     assert attend(nq, ws_bytes=1 << 20) == INV and b"WORKSPACE" in nq.lib.nq_last_error()
