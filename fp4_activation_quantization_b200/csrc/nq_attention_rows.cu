@@ -46,8 +46,8 @@ constexpr int kWalkWarps = 4, kChunkWarps = 8;
 constexpr float kRaise = 8.0f;      // log2 by which a score may exceed the running maximum
 constexpr float kLowest = -3.0e38f; // the maximum of no scores: below every finite one, and 0 * 2^(kLowest - kLowest) is 0
 
-constexpr int stages_of(int d) { return d == 256 ? 3 : 4; }
-constexpr size_t ring_bytes(int d, int warps) { return size_t(warps) * stages_of(d) * 18 * d; }
+constexpr int stages_of(int d) { return d == 64 ? 3 : 2; }  // pairs of atoms
+constexpr size_t ring_bytes(int d, int warps) { return size_t(warps) * stages_of(d) * 36 * d; }
 constexpr int row_pitch(int d) { return d + 4; }  // floats between rows of a warp's result in shared memory
 constexpr size_t merge_bytes(int d, int rows) { return size_t(kChunkWarps) * rows * (row_pitch(d) + 2) * 4; }
 
@@ -86,6 +86,11 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+
+template <int N>
+struct IntTag {
+  static constexpr int value = N;
+};
 
 // One request's share of the axis.
 struct Span {
@@ -345,8 +350,8 @@ __global__ void __launch_bounds__((WALK ? kWalkWarps : kChunkWarps) * 32,
   int b = s_req[WALK ? warp : 0];
   int64_t base = s_base[WALK ? warp : 0];  // where request b begins on the axis
 
-  const uint32_t ring = uint32_t(__cvta_generic_to_shared(smem)) + warp * (kStages * kAtom);
-  const uint8_t* ring_p = smem + warp * (kStages * kAtom);
+  const uint32_t ring = uint32_t(__cvta_generic_to_shared(smem)) + warp * (2 * kStages * kAtom);
+  const uint8_t* ring_p = smem + warp * (2 * kStages * kAtom);
   const float gk = __ldg(a.k_scale), gv = __ldg(a.v_scale);
   const int64_t head_bytes = int64_t(kAtom) << (a.cache.log_page - 4);
   Cut cut{};
@@ -446,11 +451,15 @@ __global__ void __launch_bounds__((WALK ? kWalkWarps : kChunkWarps) * 32,
       }
       missing = missing << 1 | (gone ? 1u : 0u);
       dst += kAtom;
-      if (dst >= ring + kStages * kAtom) dst -= kStages * kAtom;
+    };
+    auto issue_pair = [&]() {
+      issue();
+      issue();
+      if (dst >= ring + 2 * kStages * kAtom) dst -= 2 * kStages * kAtom;
       cp_async_commit();
     };
 #pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) issue();
+    for (int i = 0; i < kStages - 1; ++i) issue_pair();
 
     // Query fragments: lane (n = r, j) holds row n's dimensions [j D/4, (j+1) D/4) of each 8-row tile.
     uint32_t qf[NT][D / 16][2];
@@ -520,11 +529,8 @@ __global__ void __launch_bounds__((WALK ? kWalkWarps : kChunkWarps) * 32,
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[mt][nt][i] = 0.0f;
 
-    // One atom of 16 keys from t on; MASKED where some row does not see all of them.
-    auto step = [&](const uint8_t* atom, int t, auto masked_tag) {
-      constexpr bool MASKED = decltype(masked_tag)::value;
-      // ---- S^T = K' q^T
-      float sc[NT][4];
+    // ---- S^T = K' q^T of one atom
+    auto scores = [&](const uint8_t* atom, float (&sc)[NT][4]) {
       uint32_t ksw[(2 * kN + 3) / 4];  // the lane's 2 kN key scales
       if constexpr (kN == 1) {
         ksw[0] = *reinterpret_cast<const uint16_t*>(atom + KvAtom<D>::kKScales + lane * 2);
@@ -569,31 +575,24 @@ __global__ void __launch_bounds__((WALK ? kWalkWarps : kChunkWarps) * 32,
                   qf[nt][4 * c + 2 * x + y][1], c + x + y == 0);
         }
 
-      // ---- softmax over the atom's tokens t + r (x = 0, 1) and t + r + 8 (x = 2, 3)
-      if constexpr (MASKED) {
+    };
+    // ---- softmax over N atoms' tokens t + r (x = 0, 1) and t + r + 8 (x = 2, 3): scores to weights
+    auto weights = [&](auto n_tag, float (*sc)[NT][4], uint32_t (*pf)[NT][2]) {
+      constexpr int N = decltype(n_tag)::value;
+      bool raise = false;
+#pragma unroll
+      for (int n = 0; n < N; ++n)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const int key = t + r + (x >> 1) * 8;
-            if (key < lo[nt][x & 1] || key >= hi[nt][x & 1]) sc[nt][x] = -INFINITY;
-          }
-      }
-      float arg[NT][4];  // log2 of the weights
-      bool raise = false;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          arg[nt][x] = __fmaf_rn(sc[nt][x], cs[nt][x & 1], -m[nt][x & 1]);
-          raise |= arg[nt][x] > kRaise;
-        }
+          for (int x = 0; x < 4; ++x) raise |= __fmaf_rn(sc[n][nt][x], cs[nt][x & 1], -m[nt][x & 1]) > kRaise;
       if (__any_sync(kFull, raise)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
-            float top = fmaxf(sc[nt][y], sc[nt][y + 2]);
+            float top = fmaxf(sc[0][nt][y], sc[0][nt][y + 2]);
+            if (N == 2) top = fmaxf(top, fmaxf(sc[N - 1][nt][y], sc[N - 1][nt][y + 2]));
 #pragma unroll
             for (int w = 4; w < 32; w <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, w));
             if (__fmaf_rn(top, cs[nt][y], -m[nt][y]) > kRaise) {  // a row's results do not depend on its neighbours'
@@ -603,25 +602,26 @@ __global__ void __launch_bounds__((WALK ? kWalkWarps : kChunkWarps) * 32,
               l[nt][y] *= f;
 #pragma unroll
               for (int mt = 0; mt < D / 16; ++mt) o[mt][nt][y] *= f, o[mt][nt][y + 2] *= f;
-              arg[nt][y] = __fmaf_rn(sc[nt][y], cs[nt][y], -top);
-              arg[nt][y + 2] = __fmaf_rn(sc[nt][y + 2], cs[nt][y], -top);
             }
           }
       }
-      uint32_t pf[NT][2];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float p[4];
+      for (int n = 0; n < N; ++n)
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          p[x] = ex2(arg[nt][x]);
-          l[nt][x & 1] += p[x];
+        for (int nt = 0; nt < NT; ++nt) {
+          float p[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            p[x] = ex2(__fmaf_rn(sc[n][nt][x], cs[nt][x & 1], -m[nt][x & 1]));
+            l[nt][x & 1] += p[x];
+          }
+          pf[n][nt][0] = transpose8x8(pack_f16x2(p[0], p[1]));
+          pf[n][nt][1] = transpose8x8(pack_f16x2(p[2], p[3]));
         }
-        pf[nt][0] = transpose8x8(pack_f16x2(p[0], p[1]));
-        pf[nt][1] = transpose8x8(pack_f16x2(p[2], p[3]));
-      }
-
-      // ---- O^T += V'^T P^T: tokens 2j, 2j+1 (pair 0) and 2j+8, 2j+9 (pair 1), dimensions [r D/8, (r+1) D/8)
+    };
+    // ---- one atom's O^T += V'^T P^T: tokens 2j, 2j+1 (pair 0) and 2j+8, 2j+9 (pair 1), dimensions
+    // [r D/8, (r+1) D/8); keys: tokens of the atom that exist
+    auto values = [&](const uint8_t* atom, const uint32_t (&pf)[NT][2], int keys) {
       uint32_t vs2[2][kW];  // scale pairs (token, next token) of each block
       {
         uint32_t w[kW];
@@ -629,13 +629,13 @@ __global__ void __launch_bounds__((WALK ? kWalkWarps : kChunkWarps) * 32,
         for (int x = 0; x < kW; ++x)
           w[x] = *reinterpret_cast<const uint32_t*>(atom + KvAtom<D>::kVScales +
                                                     ((D == 64 ? r >> 1 : r) * 4 + j) * (4 * kW) + 4 * x);
-        if (MASKED && t + 16 > s.kv_len) {
+        if (keys < 16) {
           // Bytes behind the last key are whatever the page held: their scales
           // become zero, so that 0 * NaN cannot reach the sum.
 #pragma unroll
           for (int x = 0; x < 4 * kW; ++x) {
             const int i4 = x / kW;
-            if (t + 8 * (i4 >> 1) + 2 * j + (i4 & 1) >= s.kv_len) w[x >> 2] &= ~(0xFFu << (8 * (x & 3)));
+            if (8 * (i4 >> 1) + 2 * j + (i4 & 1) >= keys) w[x >> 2] &= ~(0xFFu << (8 * (x & 3)));
           }
         }
         if constexpr (kW == 1) {
@@ -683,25 +683,48 @@ __global__ void __launch_bounds__((WALK ? kWalkWarps : kChunkWarps) * 32,
 
     // Atoms [i_lo, i_hi) are seen whole by every row.
     const int i_lo = lo_full > t0 ? (lo_full - t0 + 15) >> 4 : 0;
-    const int i_hi = max(i_lo, hi_full > t0 ? (hi_full - t0) >> 4 : 0);
+    const int i_hi = hi_full > t0 ? min(n_atoms, (hi_full - t0) >> 4) : 0;
     const uint8_t* atom = ring_p;
-    int t = t0;
 #pragma unroll 1
-    for (int i = 0; i < n_atoms; ++i) {
-      cp_async_wait<kStages - 2>();
-      __syncwarp();  // all lanes' copies of atom i have landed, and all have read atom i - 1
-      const bool absent = (missing >> (kStages - 2)) & 1u;
-      issue();
-      if (absent) {
-        if (lane == 0) atomicOr(a.err, kErrSlot);
-      } else if (uint32_t(i - i_lo) < uint32_t(i_hi - i_lo)) {
-        step(atom, t, BoolTag<false>{});
+    for (int i = 0; i < n_atoms; i += 2) {
+      __syncwarp();  // all lanes have read the pair before
+      issue_pair();
+      cp_async_wait<kStages - 1>();
+      __syncwarp();  // all lanes' copies of this pair have landed
+      const uint32_t absent = (missing >> (2 * kStages - 2)) & 3u;  // bit 1: the first atom
+      if (i >= i_lo && i + 2 <= i_hi && absent == 0) {
+        // Two atoms at a time: two independent chains of products, one vote.
+        float sc[2][NT][4];
+        uint32_t pf[2][NT][2];
+        scores(atom, sc[0]);
+        scores(atom + kAtom, sc[1]);
+        weights(IntTag<2>{}, sc, pf);
+        values(atom, pf[0], 16);
+        values(atom + kAtom, pf[1], 16);
       } else {
-        step(atom, t, BoolTag<true>{});
+#pragma unroll 1
+        for (int h = 0; h < 2 && i + h < n_atoms; ++h) {
+          const int t = t0 + 16 * (i + h);
+          if ((absent >> (1 - h)) & 1u) {
+            if (lane == 0) atomicOr(a.err, kErrSlot);
+            continue;
+          }
+          float sc[1][NT][4];
+          uint32_t pf[1][NT][2];
+          scores(atom + h * kAtom, sc[0]);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const int key = t + r + (x >> 1) * 8;
+              if (key < lo[nt][x & 1] || key >= hi[nt][x & 1]) sc[0][nt][x] = -INFINITY;
+            }
+          weights(IntTag<1>{}, sc, pf);
+          values(atom + h * kAtom, pf[0], s.kv_len - t);
+        }
       }
-      t += 16;
-      atom += kAtom;
-      if (atom == ring_p + kStages * kAtom) atom = ring_p;
+      atom += 2 * kAtom;
+      if (atom == ring_p + 2 * kStages * kAtom) atom = ring_p;
     }
     cp_async_wait<0>();
     __syncwarp();
