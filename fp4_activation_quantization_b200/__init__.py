@@ -51,7 +51,7 @@ FLAG_SCALES_COL_MAJOR = 1 << 7
 FLAG_SCALES_PACKED_UE8M0 = 1 << 8
 FLAG_NONCAUSAL = 1 << 9
 NQ_KV_MAX_REQUESTS = 16384
-ATTENTION_WORKSPACE_BYTES = 32 << 20
+ATTENTION_WORKSPACE_BYTES = 64 << 20
 OP_RMS_DYN_FP8, OP_RMS_STATIC_FP8, OP_LN_STATIC_FP8, OP_RMS_NVFP4, OP_RMS_GROUP_FP8 = 0, 1, 2, 3, 4
 
 

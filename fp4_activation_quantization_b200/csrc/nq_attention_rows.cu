@@ -51,13 +51,28 @@ constexpr size_t ring_bytes(int d, int warps) { return size_t(warps) * stages_of
 constexpr int row_pitch(int d) { return d + 4; }  // floats between rows of a warp's result in shared memory
 constexpr size_t merge_bytes(int d, int rows) { return size_t(kChunkWarps) * rows * (row_pitch(d) + 2) * 4; }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
 }
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+__device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+// Waits for the phase of the given parity; false when the limit runs out (no wait of a sound run comes near it).
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
+  for (int i = 0; i < (1 << 22); ++i) {
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(ok)
+                 : "r"(bar), "r"(parity)
+                 : "memory");
+    if (ok) return true;
+  }
+  return false;
+}
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
+               "r"(bytes), "r"(bar)
+               : "memory");
 }
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -122,13 +137,14 @@ struct __align__(16) Cut {
   int32_t valid, q0, row0, rows;   // first query row of the request, first row and rows of the tile
   int32_t head, last, pad0, pad1;  // kv head, last part
 };
-// The workspace: counters of the chunked segments (zero between calls); for the
-// walk [0] the number of parts and, from there on, the cuts; then the parts'
-// slots, each of R rows of D floats and R pairs (maximum, sum).
+// The workspace: counters of the chunked segments and, the last of them, of the
+// parts that the walk's warps have claimed (zero between calls); for the walk the
+// number of parts and the cuts; then the parts' slots, each of R rows of D floats and R pairs (maximum, sum).
 __device__ __forceinline__ uint32_t* counters_of(const AttnArgs& a) { return reinterpret_cast<uint32_t*>(a.workspace); }
 __device__ __forceinline__ int32_t* parts_of(const AttnArgs& a) {
   return reinterpret_cast<int32_t*>(a.workspace + kAttnCounterBytes);
 }
+__device__ __forceinline__ uint32_t* claims_of(const AttnArgs& a) { return counters_of(a) + kAttnCounterBytes / 4 - 1; }
 __device__ __forceinline__ Cut* cuts_of(const AttnArgs& a) {
   return reinterpret_cast<Cut*>(a.workspace + kAttnCounterBytes + 64);
 }
@@ -252,13 +268,19 @@ __global__ void __launch_bounds__((WALK ? kWalkWarps : kChunkWarps) * 32,
   constexpr int kAtom = KvAtom<D>::kBytes;
   constexpr int kPitch = row_pitch(D);
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int64_t s_scan[kWarps], s_base[kWarps];
-  __shared__ int s_req[kWarps], s_last;
+  __shared__ int64_t s_scan[kWarps], s_before[kThreads];
+  __shared__ int s_last;
+  __shared__ __align__(8) uint64_t s_bar[kWarps][kStages];  // a pair of atoms has landed
 
   const int tid = int(threadIdx.x), lane = tid & 31, warp = tid >> 5;
   const int r = lane >> 2, j = lane & 3;
   const int heads = a.cache.heads;
 
+  const uint32_t bars = uint32_t(__cvta_generic_to_shared(s_bar[warp]));
+  if (lane == 0) {
+    for (int i = 0; i < kStages; ++i) mbar_init(bars + 8 * i, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
   griddep_wait();
   griddep_launch_dependents();
 
@@ -293,17 +315,29 @@ __global__ void __launch_bounds__((WALK ? kWalkWarps : kChunkWarps) * 32,
   }
   int64_t total = scan(mine, &before);
 
-  // WALK: shares of the axis, one a warp, of two atoms or more; few shares go to
-  // a warp of every CTA first.  Else: chunks of `chunk` atoms that no segment
-  // shares, one a CTA.
-  int parts = 0, chunk = 0;
-  auto part_of_warp = [&](int w) {
-    return parts == int(gridDim.x) * kWarps ? int(blockIdx.x) * kWarps + w : w * int(gridDim.x) + int(blockIdx.x);
+  // WALK: parts of the axis.  The first four fifths are one part a warp (of two
+  // atoms or more); the rest, as many small ones, go to whoever is free:
+  // the warps of an SM do not advance alike, and with equal shares alone the last
+  // one was done a seventh after the average.  Else: chunks of `chunk` atoms that
+  // no segment shares, one a CTA.
+  int fixed = 0, parts = 0, chunk = 0;
+  int64_t fixed_end = 0;
+  auto start_of = [&](int p) {
+    return p <= fixed ? quotient(fixed_end * p, fixed) : fixed_end + quotient((total - fixed_end) * (p - fixed), parts - fixed);
   };
-  auto start_of = [&](int64_t p) { return quotient(total * p, parts); };
-  auto owner_of = [&](int64_t u) { return int(quotient((u + 1) * parts - 1, total)); };
+  auto owner_of = [&](int64_t u) {
+    return u < fixed_end ? int(quotient((u + 1) * fixed - 1, fixed_end))
+                         : fixed + int(quotient((u - fixed_end + 1) * (parts - fixed) - 1, total - fixed_end));
+  };
   if constexpr (WALK) {
-    parts = int(min(int64_t(gridDim.x) * kWarps, (total + 1) >> 1));
+    const int64_t warps = int64_t(gridDim.x) * kWarps;
+    fixed = int(min(warps, (total + 1) >> 1));
+    fixed_end = total;
+    parts = fixed;
+    if (fixed == warps && total >= 20 * warps) {  // small parts of four atoms or more
+      fixed_end = total / 5 * 4;
+      parts = 2 * fixed;
+    }
     if (blockIdx.x == 0 && tid == 0) *parts_of(a) = parts;
   } else {
     int64_t unused;
@@ -319,45 +353,48 @@ __global__ void __launch_bounds__((WALK ? kWalkWarps : kChunkWarps) * 32,
     total = scan(mine, &before);
   }
   auto units_of = [&](const Span& s) { return WALK ? s.units : (s.units + chunk - 1) / chunk; };  // of the axis, per segment
-  if (mine > 0) {
-#pragma unroll
-    for (int w = 0; w < (WALK ? kWarps : 1); ++w) {
-      const int p = WALK ? part_of_warp(w) : int(blockIdx.x);
-      if (WALK && p >= parts) continue;
-      const int64_t u = WALK ? start_of(p) : p;
-      if (u < before || u >= before + mine) continue;
-      int64_t at = before;
-      int b = b_lo;
-      for (; b < b_hi; ++b) {
-        const Span s = span_of<R>(a, b);
-        const int64_t n = int64_t(s.tiles) * heads * units_of(s);
-        if (u < at + n) break;
-        at += n;
-      }
-      s_req[w] = b;
-      s_base[w] = at;
-    }
-  }
+  s_before[tid] = before;
   __syncthreads();
-  int part = WALK ? part_of_warp(warp) : int(blockIdx.x);
-  int64_t u0 = 0, u1 = 0;  // this warp's (CTA's) share of the axis
-  if constexpr (WALK) {
-    if (part < parts) u0 = start_of(part), u1 = start_of(part + 1);
-  } else {
-    if (part >= total) return;
-    u0 = part, u1 = part + 1;
-  }
-  int b = s_req[WALK ? warp : 0];
-  int64_t base = s_base[WALK ? warp : 0];  // where request b begins on the axis
+  int part = int(blockIdx.x) + (WALK ? warp * int(gridDim.x) : 0);
+  if (WALK ? part >= fixed : part >= total) return;
+  int b;
+  int64_t base;  // where request b begins on the axis
+  // The first request of the run of requests in which position u lies.
+  auto locate = [&](int64_t u) {
+    int i = -1;
+#pragma unroll
+    for (int q = 0; q < kWarps; ++q) i += __popc(__ballot_sync(kFull, s_before[q * 32 + lane] <= u));
+    b = i * per;
+    base = s_before[i];
+  };
 
   const uint32_t ring = uint32_t(__cvta_generic_to_shared(smem)) + warp * (2 * kStages * kAtom);
   const uint8_t* ring_p = smem + warp * (2 * kStages * kAtom);
   const float gk = __ldg(a.k_scale), gv = __ldg(a.v_scale);
   const int64_t head_bytes = int64_t(kAtom) << (a.cache.log_page - 4);
-  Cut cut{};
+  // The ring: slots in turn, their parity changes with every turn; all is read at a segment's end.
+  int wr_slot = 0, rd_slot = 0;
+  uint32_t rd_parity = 0;
 
+  int64_t u0, u1;  // this part
+  if constexpr (WALK) u0 = start_of(part), u1 = start_of(part + 1);
+  else u0 = part, u1 = part + 1;
   int64_t u = u0;
-  while (u < u1) {
+  locate(u);
+  Cut cut{};
+  while (true) {
+    if constexpr (WALK) {
+      if (u >= u1) {  // the part's end
+        if (lane == 0) cuts_of(a)[part] = cut;
+        if (parts == fixed) return;
+        if (lane == 0) part = fixed + int(atomicAdd(claims_of(a), 1u));
+        part = __shfl_sync(kFull, part, 0);
+        if (part >= parts) return;
+        u0 = u = start_of(part), u1 = start_of(part + 1);
+        locate(u);
+        cut = Cut{};
+      }
+    }
     Span s = span_of<R>(a, b);
     while (base + int64_t(s.tiles) * heads * units_of(s) <= u) {  // the next request that has rows
       base += int64_t(s.tiles) * heads * units_of(s);
@@ -421,44 +458,61 @@ __global__ void __launch_bounds__((WALK ? kWalkWarps : kChunkWarps) * 32,
     const int t0 = max(s.first + 16 * ua, lo_all & ~15), t1 = min(s.first + 16 * ub, hi_all);
     const int n_atoms = t0 < t1 ? (t1 - t0 + 15) >> 4 : 0;
     const int32_t* table = a.table + int64_t(b) * a.ld_table;
-    const uint8_t* const base_lane = a.cache.base + head * head_bytes + 16 * lane;
+    const uint8_t* const base_head = a.cache.base + head * head_bytes;
     const int page_atoms = 1 << (a.cache.log_page - 4);
-    // Atoms are issued in order: within a page the source only moves on.
-    int page_i = (t0 >> a.cache.log_page) - 1, page_end = n_atoms > 0 ? (t1 - 1) >> a.cache.log_page : -1;
+    // Atoms are issued in order, a pair to a slot: within a page the source only
+    // moves on and a pair is one copy.
+    int page_i = t0 >> a.cache.log_page;
+    const int page_end = n_atoms > 0 ? (t1 - 1) >> a.cache.log_page : -1;
     auto page_at = [&](int i) { return i <= page_end ? __ldg(table + i) : 0; };
-    int next_page = page_at(page_i + 1), left = 0, to_issue = n_atoms;
-    const uint8_t* src = nullptr;
-    bool gone = false;
-    uint32_t missing = 0, dst = ring + 16 * lane;  // missing, bit i: the atom issued i + 1 calls ago has no page
-    auto issue = [&]() {
-      if (to_issue > 0) {
-        if (left == 0) {
-          const int in = page_end >= 0 && src == nullptr ? (t0 >> 4) & (page_atoms - 1) : 0;
-          gone = uint32_t(next_page) >= uint32_t(a.cache.pages);
-          src = base_lane + int64_t(next_page) * a.cache.page_stride + in * kAtom;
-          left = page_atoms - in;
-          ++page_i;
-          next_page = page_at(page_i + 1);
-        }
-        if (!gone) {
-#pragma unroll
-          for (int x = 0; x < (kAtom / 16 + 31) / 32; ++x)
-            if (kAtom / 16 % 32 == 0 || x * 32 + lane < kAtom / 16) cp_async16(dst + 512 * x, src + 512 * x);
-        }
-        src += kAtom;
-        --left;
-        --to_issue;
-      }
-      missing = missing << 1 | (gone ? 1u : 0u);
-      dst += kAtom;
+    int page = page_at(page_i), next_page = page_at(page_i + 1);
+    int skip = (t0 >> 4) & (page_atoms - 1);  // atoms of the first page before the share
+    int left = page_atoms - skip, to_issue = n_atoms;
+    bool gone = uint32_t(page) >= uint32_t(a.cache.pages);
+    const uint8_t* src = base_head + int64_t(page) * a.cache.page_stride + skip * kAtom;
+    uint32_t missing = 0;  // bit i: the atom issued i + 1 calls ago has no page
+    auto turn_page = [&]() {
+      page = next_page;
+      ++page_i;
+      next_page = page_at(page_i + 1);
+      left = page_atoms;
+      gone = uint32_t(page) >= uint32_t(a.cache.pages);
+      src = base_head + int64_t(page) * a.cache.page_stride;
     };
     auto issue_pair = [&]() {
-      issue();
-      issue();
-      if (dst >= ring + 2 * kStages * kAtom) dst -= 2 * kStages * kAtom;
-      cp_async_commit();
-    };
+      missing <<= 2;
+      if (to_issue <= 0) return;
+      const uint32_t bar = bars + 8 * wr_slot, dst = ring + wr_slot * (2 * kAtom);
+      if (left >= 2 && to_issue >= 2 && !gone) {
+        if (lane == 0) {
+          mbar_expect(bar, 2 * kAtom);
+          bulk_copy(dst, src, 2 * kAtom, bar);
+        }
+        src += 2 * kAtom;
+        left -= 2;
+      } else {
+        uint32_t bytes = 0;
+        const uint8_t* from[2] = {nullptr, nullptr};
 #pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (h >= to_issue) break;
+          if (left == 0) turn_page();
+          if (!gone) from[h] = src, bytes += kAtom;
+          else missing |= 2u >> h;
+          src += kAtom;
+          --left;
+        }
+        if (lane == 0) {
+          mbar_expect(bar, bytes);
+          if (from[0]) bulk_copy(dst, from[0], kAtom, bar);
+          if (from[1]) bulk_copy(dst + kAtom, from[1], kAtom, bar);
+        }
+      }
+      if (left == 0) turn_page();
+      to_issue -= 2;
+      if (++wr_slot == kStages) wr_slot = 0;
+    };
+#pragma unroll 1
     for (int i = 0; i < kStages - 1; ++i) issue_pair();
 
     // Query fragments: lane (n = r, j) holds row n's dimensions [j D/4, (j+1) D/4) of each 8-row tile.
@@ -529,52 +583,61 @@ __global__ void __launch_bounds__((WALK ? kWalkWarps : kChunkWarps) * 32,
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[mt][nt][i] = 0.0f;
 
-    // ---- S^T = K' q^T of one atom
-    auto scores = [&](const uint8_t* atom, float (&sc)[NT][4]) {
-      uint32_t ksw[(2 * kN + 3) / 4];  // the lane's 2 kN key scales
-      if constexpr (kN == 1) {
-        ksw[0] = *reinterpret_cast<const uint16_t*>(atom + KvAtom<D>::kKScales + lane * 2);
-      } else {
+    // ---- S^T = K' q^T of N atoms, their products taking turns
+    auto scores = [&](auto n_tag, const uint8_t* atom, float (*sc)[NT][4]) {
+      constexpr int N = decltype(n_tag)::value;
+      uint32_t kw[N][2][kN][2];  // codes of rows r and r + 8
+      uint32_t ks2[N][2 * kN];   // each scale in both halves of an f16 pair
 #pragma unroll
-        for (int x = 0; x < kN / 2; ++x)
-          ksw[x] = *reinterpret_cast<const uint32_t*>(atom + KvAtom<D>::kKScales + lane * 2 * kN + 4 * x);
-      }
-      uint32_t kw[2][kN][2];  // codes of rows r and r + 8
+      for (int n = 0; n < N; ++n) {
+        const uint8_t* at = atom + n * kAtom;
+        uint32_t ksw[(2 * kN + 3) / 4];  // the lane's 2 kN key scales
+        if constexpr (kN == 1) {
+          ksw[0] = *reinterpret_cast<const uint16_t*>(at + KvAtom<D>::kKScales + lane * 2);
+        } else {
 #pragma unroll
-      for (int pl = 0; pl < kN; ++pl) {
-        const uint4 w = *reinterpret_cast<const uint4*>(atom + pl * 512 + lane * 16);
-        kw[(2 * pl) / kN][(2 * pl) % kN][0] = w.x;
-        kw[(2 * pl) / kN][(2 * pl) % kN][1] = w.y;
-        kw[(2 * pl + 1) / kN][(2 * pl + 1) % kN][0] = w.z;
-        kw[(2 * pl + 1) / kN][(2 * pl + 1) % kN][1] = w.w;
-      }
-      uint32_t ks2[2 * kN];  // each scale in both halves of an f16 pair
+          for (int x = 0; x < kN / 2; ++x)
+            ksw[x] = *reinterpret_cast<const uint32_t*>(at + KvAtom<D>::kKScales + lane * 2 * kN + 4 * x);
+        }
 #pragma unroll
-      for (int x = 0; x < kN; ++x) {
-        const uint32_t h = e4m3x2_to_f16x2(ksw[x / 2] >> (16 * (x % 2)));
-        ks2[2 * x] = __byte_perm(h, h, 0x1010);
-        ks2[2 * x + 1] = __byte_perm(h, h, 0x3232);
+        for (int pl = 0; pl < kN; ++pl) {
+          const uint4 w = *reinterpret_cast<const uint4*>(at + pl * 512 + lane * 16);
+          kw[n][(2 * pl) / kN][(2 * pl) % kN][0] = w.x;
+          kw[n][(2 * pl) / kN][(2 * pl) % kN][1] = w.y;
+          kw[n][(2 * pl + 1) / kN][(2 * pl + 1) % kN][0] = w.z;
+          kw[n][(2 * pl + 1) / kN][(2 * pl + 1) % kN][1] = w.w;
+        }
+#pragma unroll
+        for (int x = 0; x < kN; ++x) {
+          const uint32_t h = e4m3x2_to_f16x2(ksw[x / 2] >> (16 * (x % 2)));
+          ks2[n][2 * x] = __byte_perm(h, h, 0x1010);
+          ks2[n][2 * x + 1] = __byte_perm(h, h, 0x3232);
+        }
       }
 #pragma unroll
       for (int c = 0; c < kN; ++c)
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          uint32_t ha[4], hb[4];
-          e2m1x8_to_f16x2(kw[0][c][x], ha);
-          e2m1x8_to_f16x2(kw[1][c][x], hb);
+          uint32_t ha[N][4], hb[N][4];
 #pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            ha[y] = mul_f16x2(ha[y], ks2[c]);
-            hb[y] = mul_f16x2(hb[y], ks2[kN + c]);
+          for (int n = 0; n < N; ++n) {
+            e2m1x8_to_f16x2(kw[n][0][c][x], ha[n]);
+            e2m1x8_to_f16x2(kw[n][1][c][x], hb[n]);
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              ha[n][y] = mul_f16x2(ha[n][y], ks2[n][c]);
+              hb[n][y] = mul_f16x2(hb[n][y], ks2[n][kN + c]);
+            }
           }
 #pragma unroll
           for (int y = 0; y < 2; ++y)
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-              mma(sc[nt], ha[2 * y], hb[2 * y], ha[2 * y + 1], hb[2 * y + 1], qf[nt][4 * c + 2 * x + y][0],
-                  qf[nt][4 * c + 2 * x + y][1], c + x + y == 0);
+            for (int n = 0; n < N; ++n)
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+                mma(sc[n][nt], ha[n][2 * y], hb[n][2 * y], ha[n][2 * y + 1], hb[n][2 * y + 1],
+                    qf[nt][4 * c + 2 * x + y][0], qf[nt][4 * c + 2 * x + y][1], c + x + y == 0);
         }
-
     };
     // ---- softmax over N atoms' tokens t + r (x = 0, 1) and t + r + 8 (x = 2, 3): scores to weights
     auto weights = [&](auto n_tag, float (*sc)[NT][4], uint32_t (*pf)[NT][2]) {
@@ -684,20 +747,22 @@ __global__ void __launch_bounds__((WALK ? kWalkWarps : kChunkWarps) * 32,
     // Atoms [i_lo, i_hi) are seen whole by every row.
     const int i_lo = lo_full > t0 ? (lo_full - t0 + 15) >> 4 : 0;
     const int i_hi = hi_full > t0 ? min(n_atoms, (hi_full - t0) >> 4) : 0;
-    const uint8_t* atom = ring_p;
 #pragma unroll 1
     for (int i = 0; i < n_atoms; i += 2) {
       __syncwarp();  // all lanes have read the pair before
       issue_pair();
-      cp_async_wait<kStages - 1>();
-      __syncwarp();  // all lanes' copies of this pair have landed
+      const uint8_t* atom = ring_p + rd_slot * (2 * kAtom);
+      if (!mbar_wait(bars + 8 * rd_slot, rd_parity)) {
+        // Never in a sound run: the results of this call are not valid.
+        if (lane == 0) atomicOr(a.err, kErrWait);
+      }
+      if (++rd_slot == kStages) rd_slot = 0, rd_parity ^= 1;
       const uint32_t absent = (missing >> (2 * kStages - 2)) & 3u;  // bit 1: the first atom
       if (i >= i_lo && i + 2 <= i_hi && absent == 0) {
         // Two atoms at a time: two independent chains of products, one vote.
         float sc[2][NT][4];
         uint32_t pf[2][NT][2];
-        scores(atom, sc[0]);
-        scores(atom + kAtom, sc[1]);
+        scores(IntTag<2>{}, atom, sc);
         weights(IntTag<2>{}, sc, pf);
         values(atom, pf[0], 16);
         values(atom + kAtom, pf[1], 16);
@@ -711,7 +776,7 @@ __global__ void __launch_bounds__((WALK ? kWalkWarps : kChunkWarps) * 32,
           }
           float sc[1][NT][4];
           uint32_t pf[1][NT][2];
-          scores(atom + h * kAtom, sc[0]);
+          scores(IntTag<1>{}, atom + h * kAtom, sc);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -723,10 +788,7 @@ __global__ void __launch_bounds__((WALK ? kWalkWarps : kChunkWarps) * 32,
           values(atom + h * kAtom, pf[0], s.kv_len - t);
         }
       }
-      atom += 2 * kAtom;
-      if (atom == ring_p + 2 * kStages * kAtom) atom = ring_p;
     }
-    cp_async_wait<0>();
     __syncwarp();
 
     // ---- the segment's end: sums over the lanes of a column
@@ -845,7 +907,6 @@ __global__ void __launch_bounds__((WALK ? kWalkWarps : kChunkWarps) * 32,
       return;
     }
   }
-  if (WALK && part < parts && lane == 0) cuts_of(a)[part] = cut;
 }
 
 // Joins the parts of a segment whose first part is blockIdx.x, if there is one.
@@ -857,6 +918,7 @@ __global__ void __launch_bounds__(kAttnJoinThreads) rows_join_kernel(const AttnA
   griddep_launch_dependents();
   const int parts = __ldcg(parts_of(a));
   const int4 c0 = __ldcg(reinterpret_cast<const int4*>(cuts_of(a) + first)), c1 = __ldcg(reinterpret_cast<const int4*>(cuts_of(a) + first) + 1);
+  if (first == 0 && threadIdx.x == 0) *claims_of(a) = 0;
   if (first >= parts || !c0.x) return;
   const Cut cut = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, 0, 0};
   join.run(a, cut.last - first + 1, [&](int p) { return slot_of<D, R>(a, 2 * int64_t(first + p) + (p == 0 ? 1 : 0)); }, cut,

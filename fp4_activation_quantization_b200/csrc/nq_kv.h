@@ -94,7 +94,7 @@ const void* kv_gather_kernel(int d, bool vec);
 constexpr int kKvPlanThreads = 512;
 constexpr int kKvCopyThreads = 256;
 
-constexpr int kAttnJoinThreads = 256;
+constexpr int kAttnJoinThreads = 128;
 struct AttnRows {
   const void* kernel;
   const void* join;  // walk: a CTA per part, after it

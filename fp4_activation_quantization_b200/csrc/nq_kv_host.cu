@@ -263,7 +263,7 @@ nq_status nq_attention_nvfp4_kv(const void* q, int64_t ld_q_token, int64_t ld_q_
   if (grid <= 0) return error(NQ_ERR_CUDA, "%s: no CUDA device", fn);
   void* args[] = {&a};
   if (segments <= grid / 2) {
-    const int64_t room = (workspace_bytes - nq::kAttnHeader) / slot, counters = nq::kAttnCounterBytes / 4;
+    const int64_t room = (workspace_bytes - nq::kAttnHeader) / slot, counters = nq::kAttnCounterBytes / 4 - 1;
     grid = grid < room ? grid : room;
     grid = grid < counters ? grid : counters;
     if (segments * (atoms / 32 + 1) < grid) grid = segments * (atoms / 32 + 1);
@@ -276,13 +276,13 @@ nq_status nq_attention_nvfp4_kv(const void* q, int64_t ld_q_token, int64_t ld_q_
   grid = nq::host::resident_ctas(k.kernel, k.threads, k.smem);
   const int warps = k.threads / 32;
   if (grid <= 0) return error(NQ_ERR_CUDA, "%s: no CUDA device", fn);
-  int64_t room = (workspace_bytes - nq::kAttnHeader) / (2 * slot);
-  room = room < nq::kAttnMaxParts ? room : nq::kAttnMaxParts;
+  int64_t room = (workspace_bytes - nq::kAttnHeader) / (2 * slot) / 2;  // two parts a warp, two slots each
+  room = room < nq::kAttnMaxParts / 2 ? room : nq::kAttnMaxParts / 2;
   grid = grid < room / warps ? grid : room / warps;
   nq_status s = nq::host::launch(fn, k.kernel, unsigned(grid), k.threads, k.smem, args,
                                  (flags & NQ_FLAG_PDL) != 0, static_cast<cudaStream_t>(stream));
   if (s == NQ_OK)  // may start while the first launch ends; it waits for its results
-    s = nq::host::launch(fn, k.join, unsigned(grid * warps), nq::kAttnJoinThreads, 0, args, true,
+    s = nq::host::launch(fn, k.join, unsigned(2 * grid * warps), nq::kAttnJoinThreads, 0, args, true,
                          static_cast<cudaStream_t>(stream));
   return s;
 }

@@ -371,7 +371,7 @@ nq_status nq_rmsnorm_quant_nvfp4(const void* x, int64_t ld_x, const void* residu
 /* Most requests a plan takes. */
 #define NQ_KV_MAX_REQUESTS 16384
 /* Bytes of the workspace nq_attention_nvfp4_kv needs, whatever the sizes. */
-#define NQ_ATTENTION_WORKSPACE_BYTES (32 << 20)
+#define NQ_ATTENTION_WORKSPACE_BYTES (64 << 20)
 
 /* Bytes of one page of all kv heads (the smallest page_stride):
  * kv_heads * page_size * d * 9 / 8. */
