@@ -507,80 +507,77 @@ def kv_cache_shape(num_pages: int, kv_heads: int, head_dim: int, page_size: int)
 
 
 # These calls run once per layer and decode step, where a few microseconds of
-# argument checks would be the cost of the call: each tensor is asked for its
-# device, type, shape and strides once, and the current stream is read without
-# building a Stream object.
-def _launch(index: int, name: str, args, stream) -> None:
-    """Call ``name`` on device ``index``, the stream last; the device is switched to only when it is another one."""
-    if torch._C._cuda_getDevice() == index:
-        if stream is None:
-            stream = torch._C._cuda_getCurrentRawStream(index)
-        status = getattr(_get_lib(), name)(*args, stream if type(stream) is int else _stream(stream))
+# argument checks would be the cost of the call.  Each first asks its tensors, in
+# plain attribute reads, whether they are what it takes; only when one is not does
+# it look for the one to name in the error.
+_f32, _i32, _i64, _u8, _bf16 = torch.float32, torch.int32, torch.int64, torch.uint8, torch.bfloat16
+_functions: dict = {}
+
+
+def _launch(dev: int, name: str, args, stream) -> None:
+    """Call ``name`` on CUDA device ``dev``, the stream last; the device is switched to only when it is another one."""
+    f = _functions.get(name)
+    if f is None:
+        f = _functions[name] = getattr(_get_lib(), name)
+    if torch._C._cuda_getDevice() == dev:
+        status = f(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
     else:
-        with torch.cuda.device(index):
-            status = getattr(_get_lib(), name)(*args, _stream(stream))
-    if status != NQ_OK:
+        with torch.cuda.device(dev):
+            status = f(*args, _stream(stream))
+    if status:
         raise NQError(status, name)
 
 
-def _device(t, name: str) -> int:
-    """Index of the CUDA device that tensor t lives on."""
-    _need(isinstance(t, torch.Tensor) and t.is_cuda, f"{name} must be a CUDA tensor")
-    return t.get_device()
+def _wrong(dev, **want) -> None:
+    """Raise ValueError for the first tensor that is not (tensor, dtype, shape, contiguous); None in a shape: any."""
+    for name, (t, dtype, shape, contiguous) in want.items():
+        what = f"{name} must be a {dtype} CUDA tensor [{', '.join('*' if n is None else str(n) for n in shape)}]"
+        _need(isinstance(t, torch.Tensor) and t.is_cuda, what)
+        _need(t.dtype == dtype and t.dim() == len(shape) and all(n is None or n == m for n, m in zip(shape, t.shape)),
+              f"{what}, got {t.dtype} {tuple(t.shape)}")
+        _need(dev is None or t.get_device() == dev, f"all tensors must be on one device: {name} is not on cuda:{dev}")
+        _need(not contiguous or t.is_contiguous(), f"{name} must be contiguous")
+    raise ValueError("invalid arguments")
 
 
-def _vector(t, name: str, dtype, n, dev: int):
-    """Contiguous 1-D tensor of n elements (None: any number) on device dev; returns (length, address)."""
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.dim() == 1 and t.get_device() == dev
-            and t.is_contiguous() and (n is None or t.shape[0] == n)):
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor [{'n' if n is None else n}] on cuda:{dev}")
-    return t.shape[0], t.data_ptr()
+def _device_of(t) -> int:
+    try:
+        return t.get_device()  # -1 on the CPU
+    except AttributeError:
+        return -1
 
 
-def _one(t, name: str, dev: int) -> int:
-    if not (isinstance(t, torch.Tensor) and t.dtype is torch.float32 and t.numel() == 1 and t.get_device() == dev):
-        raise ValueError(f"{name} must be a one-element float32 tensor on cuda:{dev}")
-    return t.data_ptr()
-
-
-def _heads(t, name: str, dev: int, T=None, heads=None, d=None):
-    """bf16 [T, heads, d] on device dev, last dimension contiguous: (T, heads, d, token stride, head stride, address)."""
-    if not (isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16 and t.dim() == 3 and t.get_device() == dev):
-        raise ValueError(f"{name} must be a bfloat16 tensor [T, heads, d] on cuda:{dev}")
+def _heads(t, name: str):
+    """Token and head strides of bf16 [T, heads, d], whose last dimension has to be contiguous."""
     n, H, D = t.shape
     s0, s1, s2 = t.stride()
-    if (s2 != 1 and D > 1) or (T is not None and n != T) or (heads is not None and H != heads) or (d is not None and D != d):
-        raise ValueError(f"{name} must be [{T}, {heads}, {d}] with a contiguous last dimension, got {tuple(t.shape)} with "
-                         f"strides {t.stride()}")
+    if s2 != 1 and D > 1:
+        raise ValueError(f"{name} must have a contiguous last dimension")
     if H <= 1:
         s1 = max(s1, D)
     if n <= 1:
         s0 = max(s0, H * D, (H - 1) * s1 + D)
-    return n, H, D, s0, s1, t.data_ptr()
+    return s0, s1
 
 
-def _cache(cache, d: int, dev: int):
-    """(pages, kv heads, tokens a page, page stride, address) of a cache tensor for head dimension d."""
-    if not (isinstance(cache, torch.Tensor) and cache.dtype is torch.uint8 and cache.dim() == 3 and cache.get_device() == dev):
-        raise ValueError(f"cache must be a uint8 tensor of kv_cache_shape on cuda:{dev}")
+def _cache(cache, d: int):
+    """(pages, kv heads, tokens a page, page stride) of a cache tensor for head dimension d."""
     pages, heads, n = cache.shape
     s0, s1, s2 = cache.stride()
     if s2 != 1 or (heads > 1 and s1 != n):
         raise ValueError("cache must be contiguous within a page")
     if d < 1 or n * 8 % (9 * d):
         raise ValueError(f"cache rows of {n} bytes hold no whole tokens of head dimension {d}")
-    return pages, heads, n * 8 // (9 * d), (s0 if pages > 1 else max(s0, heads * n)), cache.data_ptr()
+    return pages, heads, n * 8 // (9 * d), (s0 if pages > 1 else max(s0, heads * n))
 
 
-def _table(t, B: int, dev: int):
-    """(columns, row stride, address) of a block table of B rows."""
-    if not (isinstance(t, torch.Tensor) and t.dtype is torch.int32 and t.dim() == 2 and t.get_device() == dev
-            and t.shape[0] == B):
-        raise ValueError(f"block_table must be an int32 tensor [{B}, pages] on cuda:{dev}")
+def _table(t, B: int):
+    """(columns, row stride) of a block table of B rows."""
     width = t.shape[1]
     s0, s1 = t.stride()
-    _need(width <= 1 or s1 == 1, "block_table must have a contiguous last dimension")
-    return width, (s0 if B > 1 else max(s0, width)), t.data_ptr()
+    if width > 1 and s1 != 1:
+        raise ValueError("block_table must have a contiguous last dimension")
+    return width, (s0 if B > 1 else max(s0, width))
 
 
 def nq_kv_plan(cached_lens, new_lens, block_table, free_pages, free_head, tokens: int, page_size: int, *,
@@ -594,24 +591,37 @@ def nq_kv_plan(cached_lens, new_lens, block_table, free_pages, free_head, tokens
     [B], positions int32 [tokens], slots int64 [tokens], free_head_out int32
     [1])``; pass ``free_head_out=free_head`` to advance the list in place.
     """
-    dev = _device(new_lens, "new_lens")
-    B, new_p = _vector(new_lens, "new_lens", torch.int32, None, dev)
-    _, cached_p = _vector(cached_lens, "cached_lens", torch.int32, B, dev)
-    width, ld, table_p = _table(block_table, B, dev)
-    n_free, free_p = _vector(free_pages, "free_pages", torch.int32, None, dev)
-    _, head_p = _vector(free_head, "free_head", torch.int32, 1, dev)
+    dev = _device_of(new_lens)
+    try:
+        B = new_lens.shape[0]
+        ok = (dev >= 0 and cached_lens.get_device() == dev and block_table.get_device() == dev
+              and free_pages.get_device() == dev and free_head.get_device() == dev
+              and new_lens.dtype is _i32 and cached_lens.dtype is _i32 and block_table.dtype is _i32
+              and free_pages.dtype is _i32 and free_head.dtype is _i32
+              and new_lens.dim() == 1 and cached_lens.shape == new_lens.shape and block_table.dim() == 2
+              and block_table.shape[0] == B and free_pages.dim() == 1 and free_head.shape == (1,)
+              and new_lens.is_contiguous() and cached_lens.is_contiguous() and free_pages.is_contiguous())
+    except (AttributeError, IndexError):
+        ok, B = False, None
+    if not ok:
+        _wrong(None if dev < 0 else dev, new_lens=(new_lens, _i32, (None,), True), cached_lens=(cached_lens, _i32, (B,), True),
+               block_table=(block_table, _i32, (B, None), False), free_pages=(free_pages, _i32, (None,), True),
+               free_head=(free_head, _i32, (1,), False))
+    width, ld = _table(block_table, B)
     _need(tokens >= 0, "tokens must not be negative")
     # One allocation for the int32 results.
-    cu_q, kv_lens, head_out, positions = torch.empty(2 * B + 2 + tokens, dtype=torch.int32, device=new_lens.device).split(
-        (B + 1, B, 1, tokens))
-    slots = torch.empty(tokens, dtype=torch.int64, device=new_lens.device)
+    buf = torch.empty(2 * B + 2 + tokens, dtype=_i32, device=new_lens.device)
+    cu_q, kv_lens, head_out, positions = buf.split((B + 1, B, 1, tokens))
+    slots = torch.empty(tokens, dtype=_i64, device=new_lens.device)
     if free_head_out is None:
         free_head_out = head_out
-    _, out_p = _vector(free_head_out, "free_head_out", torch.int32, 1, dev)
-    cu_p = cu_q.data_ptr()
-    _launch(dev, "nq_kv_plan", (cached_p, new_p, table_p, ld, width, free_p, n_free, head_p, out_p, cu_p,
-                                cu_p + 4 * (B + 1), cu_p + 4 * (2 * B + 2), slots.data_ptr(), B, tokens, page_size, flags),
-            stream)
+    elif _device_of(free_head_out) != dev or free_head_out.dtype is not _i32 or free_head_out.shape != (1,):
+        _wrong(dev, free_head_out=(free_head_out, _i32, (1,), False))
+    cu_p = buf.data_ptr()
+    _launch(dev, "nq_kv_plan", (cached_lens.data_ptr(), new_lens.data_ptr(), block_table.data_ptr(), ld, width,
+                                free_pages.data_ptr(), free_pages.shape[0], free_head.data_ptr(), free_head_out.data_ptr(),
+                                cu_p, cu_p + 4 * (B + 1), cu_p + 4 * (2 * B + 2), slots.data_ptr(), B, tokens, page_size,
+                                flags), stream)
     return cu_q, kv_lens, positions, slots, free_head_out
 
 
@@ -619,31 +629,62 @@ def nq_kv_append_nvfp4(k, v, slots, cache, k_scale, v_scale, *, flags: int = 0, 
     """Quantize keys and values (bf16 [T, kv heads, d], any token and head strides) into
     their slots (int64 [T], < 0 skips) of ``cache`` (uint8 of ``kv_cache_shape``), under
     the one-element float32 global scales ``k_scale`` and ``v_scale``."""
-    dev = _device(k, "k")
-    T, H, d, kt, kh, k_p = _heads(k, "k", dev)
-    _, _, _, vt, vh, v_p = _heads(v, "v", dev, T, H, d)
-    pages, heads, page, stride, cache_p = _cache(cache, d, dev)
-    _need(heads == H, f"cache has {heads} kv heads, k has {H}")
-    _, slots_p = _vector(slots, "slots", torch.int64, T, dev)
-    _launch(dev, "nq_kv_append_nvfp4", (k_p, kt, kh, v_p, vt, vh, slots_p, _one(k_scale, "k_scale", dev),
-                                        _one(v_scale, "v_scale", dev), cache_p, stride, pages, T, H, d, page, flags), stream)
+    dev = _device_of(k)
+    try:
+        T, H, d = k.shape
+        ok = (dev >= 0 and v.get_device() == dev and slots.get_device() == dev and cache.get_device() == dev
+              and k_scale.get_device() == dev and v_scale.get_device() == dev
+              and k.dtype is _bf16 and v.dtype is _bf16 and slots.dtype is _i64 and cache.dtype is _u8
+              and k_scale.dtype is _f32 and v_scale.dtype is _f32
+              and v.shape == k.shape and slots.shape == (T,) and cache.dim() == 3 and cache.shape[1] == H
+              and k_scale.numel() == 1 and v_scale.numel() == 1 and slots.is_contiguous())
+    except (AttributeError, ValueError, IndexError):
+        ok, T, H, d = False, None, None, None
+    if not ok:
+        _wrong(None if dev < 0 else dev, k=(k, _bf16, (T, H, d) if T is not None else (None,) * 3, False),
+               v=(v, _bf16, (T, H, d), False), slots=(slots, _i64, (T,), True), cache=(cache, _u8, (None, H, None), False),
+               k_scale=(k_scale, _f32, (1,), False), v_scale=(v_scale, _f32, (1,), False))
+    kt, kh = _heads(k, "k")
+    vt, vh = _heads(v, "v")
+    pages, _, page, stride = _cache(cache, d)
+    _launch(dev, "nq_kv_append_nvfp4", (k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, slots.data_ptr(), k_scale.data_ptr(),
+                                        v_scale.data_ptr(), cache.data_ptr(), stride, pages, T, H, d, page, flags), stream)
 
 
 def nq_kv_gather_nvfp4(cache, slots, k_scale, v_scale, head_dim: int, *, k_out=None, v_out=None, flags: int = 0,
                        stream=None):
     """Read tokens back: ``(k, v)`` bf16 [T, kv heads, head_dim] of ``slots`` (int64 [T], < 0 gives zeros)."""
-    dev = _device(cache, "cache")
-    pages, H, page, stride, cache_p = _cache(cache, head_dim, dev)
-    T, slots_p = _vector(slots, "slots", torch.int64, None, dev)
+    dev = _device_of(cache)
+    try:
+        T = slots.shape[0]
+        ok = (dev >= 0 and slots.get_device() == dev and k_scale.get_device() == dev and v_scale.get_device() == dev
+              and cache.dtype is _u8 and slots.dtype is _i64 and k_scale.dtype is _f32 and v_scale.dtype is _f32
+              and cache.dim() == 3 and slots.dim() == 1 and k_scale.numel() == 1 and v_scale.numel() == 1
+              and slots.is_contiguous())
+    except (AttributeError, IndexError):
+        ok = False
+    if not ok:
+        _wrong(None if dev < 0 else dev, cache=(cache, _u8, (None,) * 3, False), slots=(slots, _i64, (None,), True),
+               k_scale=(k_scale, _f32, (1,), False), v_scale=(v_scale, _f32, (1,), False))
+    pages, H, page, stride = _cache(cache, head_dim)
+    shape = (T, H, head_dim)
+    kt = vt = H * head_dim
+    kh = vh = head_dim
     if k_out is None:
-        k_out = torch.empty((T, H, head_dim), dtype=torch.bfloat16, device=cache.device)
+        k_out = torch.empty(shape, dtype=_bf16, device=cache.device)
+    else:
+        if _device_of(k_out) != dev or k_out.dtype is not _bf16 or k_out.shape != shape:
+            _wrong(dev, k_out=(k_out, _bf16, shape, False))
+        kt, kh = _heads(k_out, "k_out")
     if v_out is None:
-        v_out = torch.empty((T, H, head_dim), dtype=torch.bfloat16, device=cache.device)
-    _, _, _, kt, kh, k_p = _heads(k_out, "k_out", dev, T, H, head_dim)
-    _, _, _, vt, vh, v_p = _heads(v_out, "v_out", dev, T, H, head_dim)
-    _launch(dev, "nq_kv_gather_nvfp4", (cache_p, stride, pages, slots_p, _one(k_scale, "k_scale", dev),
-                                        _one(v_scale, "v_scale", dev), k_p, kt, kh, v_p, vt, vh, T, H, head_dim, page, flags),
-            stream)
+        v_out = torch.empty(shape, dtype=_bf16, device=cache.device)
+    else:
+        if _device_of(v_out) != dev or v_out.dtype is not _bf16 or v_out.shape != shape:
+            _wrong(dev, v_out=(v_out, _bf16, shape, False))
+        vt, vh = _heads(v_out, "v_out")
+    _launch(dev, "nq_kv_gather_nvfp4", (cache.data_ptr(), stride, pages, slots.data_ptr(), k_scale.data_ptr(),
+                                        v_scale.data_ptr(), k_out.data_ptr(), kt, kh, v_out.data_ptr(), vt, vh, T, H,
+                                        head_dim, page, flags), stream)
     return k_out, v_out
 
 
@@ -658,33 +699,54 @@ def nq_attention_nvfp4_kv(q, cache, block_table, kv_lens, cu_q, k_scale, v_scale
     FLAG_NONCAUSAL; ``window`` > 0 limits a row to its last ``window`` keys;
     ``scale`` defaults to d ** -0.5.  ``workspace``: a zero-filled uint8
     CUDA tensor of ATTENTION_WORKSPACE_BYTES, kept between calls that do not run
-    at the same time; without it each call makes its own.  Returns ``(out bf16 [T, heads, d], lse
-    float32 [T, heads] or None)``; rows no request owns are left as they were.
+    at the same time; without it each call makes its own.  Returns ``(out bf16
+    [T, heads, d], lse float32 [T, heads] or None)``; rows no request owns are left
+    as they were.
     """
-    dev = _device(q, "q")
-    T, heads, d, qt, qh, q_p = _heads(q, "q", dev)
-    pages, H, page, stride, cache_p = _cache(cache, d, dev)
-    B, kv_p = _vector(kv_lens, "kv_lens", torch.int32, None, dev)
-    _, cu_p = _vector(cu_q, "cu_q", torch.int32, B + 1, dev)
-    width, ld, table_p = _table(block_table, B, dev)
+    dev = _device_of(q)
+    try:
+        T, heads, d = q.shape
+        B = kv_lens.shape[0]
+        ok = (dev >= 0 and cache.get_device() == dev and block_table.get_device() == dev and kv_lens.get_device() == dev
+              and cu_q.get_device() == dev and k_scale.get_device() == dev and v_scale.get_device() == dev
+              and q.dtype is _bf16 and cache.dtype is _u8 and block_table.dtype is _i32 and kv_lens.dtype is _i32
+              and cu_q.dtype is _i32 and k_scale.dtype is _f32 and v_scale.dtype is _f32
+              and cache.dim() == 3 and block_table.dim() == 2 and block_table.shape[0] == B and kv_lens.dim() == 1
+              and cu_q.shape == (B + 1,) and k_scale.numel() == 1 and v_scale.numel() == 1
+              and kv_lens.is_contiguous() and cu_q.is_contiguous())
+    except (AttributeError, ValueError, IndexError):
+        ok, B = False, None
+    if not ok:
+        _wrong(None if dev < 0 else dev, q=(q, _bf16, (None,) * 3, False), cache=(cache, _u8, (None,) * 3, False),
+               kv_lens=(kv_lens, _i32, (None,), True), cu_q=(cu_q, _i32, (None if B is None else B + 1,), True),
+               block_table=(block_table, _i32, (B, None), False), k_scale=(k_scale, _f32, (1,), False),
+               v_scale=(v_scale, _f32, (1,), False))
+    qt, qh = _heads(q, "q")
+    pages, H, page, stride = _cache(cache, d)
+    width, ld = _table(block_table, B)
     if out is None:
-        out = torch.empty((T, heads, d), dtype=torch.bfloat16, device=q.device)
-        ot, oh, out_p = heads * d, d, out.data_ptr()
+        out = torch.empty((T, heads, d), dtype=_bf16, device=q.device)
+        ot, oh = heads * d, d
     else:
-        _, _, _, ot, oh, out_p = _heads(out, "out", dev, T, heads, d)
+        if _device_of(out) != dev or out.dtype is not _bf16 or out.shape != q.shape:
+            _wrong(dev, out=(out, _bf16, (T, heads, d), False))
+        ot, oh = _heads(out, "out")
     if want_lse and lse is None:
-        lse = torch.empty((T, heads), dtype=torch.float32, device=q.device)
+        lse = torch.empty((T, heads), dtype=_f32, device=q.device)
     lse_p, ld_lse = None, heads
     if lse is not None:
-        _need(isinstance(lse, torch.Tensor) and lse.dtype is torch.float32 and lse.shape == (T, heads)
-              and lse.get_device() == dev and (heads <= 1 or lse.stride(1) == 1),
-              f"lse must be a float32 tensor {(T, heads)} on cuda:{dev}")
-        lse_p, ld_lse = lse.data_ptr(), (lse.stride(0) if T > 1 else max(lse.stride(0), heads))
+        if _device_of(lse) != dev or lse.dtype is not _f32 or lse.shape != (T, heads):
+            _wrong(dev, lse=(lse, _f32, (T, heads), False))
+        ld_lse, s1 = lse.stride()
+        _need(heads <= 1 or s1 == 1, "lse must have a contiguous last dimension")
+        lse_p, ld_lse = lse.data_ptr(), (ld_lse if T > 1 else max(ld_lse, heads))
     if workspace is None:
-        workspace = torch.zeros(ATTENTION_WORKSPACE_BYTES, dtype=torch.uint8, device=q.device)
-    ws_n, ws_p = _vector(workspace, "workspace", torch.uint8, None, dev)
+        workspace = torch.zeros(ATTENTION_WORKSPACE_BYTES, dtype=_u8, device=q.device)
+    elif _device_of(workspace) != dev or workspace.dtype is not _u8 or workspace.dim() != 1 or not workspace.is_contiguous():
+        _wrong(dev, workspace=(workspace, _u8, (None,), True))
     _launch(dev, "nq_attention_nvfp4_kv",
-            (q_p, qt, qh, cache_p, stride, pages, table_p, ld, width, kv_p, cu_p, _one(k_scale, "k_scale", dev),
-             _one(v_scale, "v_scale", dev), out_p, ot, oh, lse_p, ld_lse, ws_p, ws_n, T, B, heads, H, d, page,
-             d ** -0.5 if scale is None else scale, window, flags), stream)
+            (q.data_ptr(), qt, qh, cache.data_ptr(), stride, pages, block_table.data_ptr(), ld, width, kv_lens.data_ptr(),
+             cu_q.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), out.data_ptr(), ot, oh, lse_p, ld_lse,
+             workspace.data_ptr(), workspace.shape[0], T, B, heads, H, d, page, d ** -0.5 if scale is None else scale, window,
+             flags), stream)
     return out, lse

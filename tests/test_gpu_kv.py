@@ -496,6 +496,24 @@ def test_binding_refusals(nq):
         nq.nq_kv_gather_nvfp4(s["cache"], torch.zeros(1, dtype=torch.int32, device="cuda"), s["gk"], s["gv"], 128)
     with pytest.raises(ValueError):
         nq.nq_kv_plan(s["kv_lens"].long(), s["kv_lens"], s["table"], s["kv_lens"], s["kv_lens"], 1, 16)
+    for name in good:  # no tensor at all
+        with pytest.raises(ValueError, match=name):
+            nq.nq_attention_nvfp4_kv(**{**good, name: None})
+    args = [s["kv_lens"], s["kv_lens"], s["table"], s["kv_lens"], s["kv_lens"]]
+    for i in range(5):
+        for bad in (None, 3, args[i].cpu(), args[i].float(), args[i][..., None]):
+            with pytest.raises(ValueError):
+                nq.nq_kv_plan(*[bad if i == j else a for j, a in enumerate(args)], 1, 16)
+    k = torch.zeros(2, 2, 128, dtype=torch.bfloat16, device="cuda")
+    args = [k, k, torch.zeros(2, dtype=torch.int64, device="cuda"), s["cache"], s["gk"], s["gv"]]
+    for i in range(6):
+        for bad in (None, args[i].cpu(), args[i].double(), args[i][None]):
+            with pytest.raises(ValueError):
+                if i >= 4 and bad is not None and bad.dtype == torch.float32 and bad.is_cuda:
+                    raise ValueError  # one element in any shape is taken
+                nq.nq_kv_append_nvfp4(*[bad if i == j else a for j, a in enumerate(args)])
+    with pytest.raises(ValueError):
+        nq.nq_kv_append_nvfp4(k.transpose(1, 2), k.transpose(1, 2), *args[2:])
 
 
 # ----------------------------------------------------------------------------------------- all of it together ----
