@@ -132,22 +132,21 @@ __device__ __forceinline__ Span span_of(const AttnArgs& a, int b) {
   return s;
 }
 
-// What the joining launch needs to know of a segment whose first part is p.
+// What the joining launch needs to know of a segment that was cut.
 struct __align__(16) Cut {
-  int32_t valid, q0, row0, rows;   // first query row of the request, first row and rows of the tile
-  int32_t head, last, pad0, pad1;  // kv head, last part
+  int32_t first, last, head, q0;  // parts, kv head, first query row of the request
+  int32_t row0, rows, pad0, pad1;  // first row and rows of the tile
 };
-// The workspace: counters of the chunked segments and, the last of them, of the
-// parts that the walk's warps have claimed (zero between calls); for the walk the
-// number of parts and the cuts; then the parts' slots, each of R rows of D floats and R pairs (maximum, sum).
+// The workspace: counters, zero between calls: of the chunked segments and, the
+// last three of them, of the walk's claimed parts, its cuts and the joining CTAs
+// that are done; then the cuts, in any order, and the parts' slots, each of R rows
+// of D floats and R pairs (maximum, sum).
 __device__ __forceinline__ uint32_t* counters_of(const AttnArgs& a) { return reinterpret_cast<uint32_t*>(a.workspace); }
-__device__ __forceinline__ int32_t* parts_of(const AttnArgs& a) {
-  return reinterpret_cast<int32_t*>(a.workspace + kAttnCounterBytes);
+enum WalkCounter { kClaims = 1, kCuts, kDone };
+__device__ __forceinline__ uint32_t* counter_of(const AttnArgs& a, WalkCounter c) {
+  return counters_of(a) + kAttnCounterBytes / 4 - c;
 }
-__device__ __forceinline__ uint32_t* claims_of(const AttnArgs& a) { return counters_of(a) + kAttnCounterBytes / 4 - 1; }
-__device__ __forceinline__ Cut* cuts_of(const AttnArgs& a) {
-  return reinterpret_cast<Cut*>(a.workspace + kAttnCounterBytes + 64);
-}
+__device__ __forceinline__ Cut* cuts_of(const AttnArgs& a) { return reinterpret_cast<Cut*>(a.workspace + kAttnCounterBytes); }
 template <int D, int R>
 __device__ __forceinline__ float* slot_of(const AttnArgs& a, int64_t i) {
   return reinterpret_cast<float*>(a.workspace + kAttnHeader) + i * (R * (D + 2));
@@ -183,6 +182,7 @@ struct Join {
     float4 x[kE];
 #pragma unroll
     for (int e = 0; e < kE; ++e) x[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    __syncthreads();  // a tile joined before has been written out
     if (tid < R) top[tid] = kLowest, l[tid] = 0.0f;
     for (int p0 = 0; p0 < n; p0 += kMax) {
       const int here = min(kMax, n - p0);
@@ -338,7 +338,6 @@ __global__ void __launch_bounds__((WALK ? kWalkWarps : kChunkWarps) * 32,
       fixed_end = total / 5 * 4;
       parts = 2 * fixed;
     }
-    if (blockIdx.x == 0 && tid == 0) *parts_of(a) = parts;
   } else {
     int64_t unused;
     const int64_t all = scan(segments, &unused);
@@ -381,18 +380,15 @@ __global__ void __launch_bounds__((WALK ? kWalkWarps : kChunkWarps) * 32,
   else u0 = part, u1 = part + 1;
   int64_t u = u0;
   locate(u);
-  Cut cut{};
   while (true) {
     if constexpr (WALK) {
       if (u >= u1) {  // the part's end
-        if (lane == 0) cuts_of(a)[part] = cut;
         if (parts == fixed) return;
-        if (lane == 0) part = fixed + int(atomicAdd(claims_of(a), 1u));
+        if (lane == 0) part = fixed + int(atomicAdd(counter_of(a, kClaims), 1u));
         part = __shfl_sync(kFull, part, 0);
         if (part >= parts) return;
         u0 = u = start_of(part), u1 = start_of(part + 1);
         locate(u);
-        cut = Cut{};
       }
     }
     Span s = span_of<R>(a, b);
@@ -831,7 +827,8 @@ __global__ void __launch_bounds__((WALK ? kWalkWarps : kChunkWarps) * 32,
         // A part: of a segment that began earlier, or of one that begins here.
         const bool begins = seg0 >= u0;
         float* slot = slot_of<D, R>(a, 2 * int64_t(part) + (begins ? 1 : 0));
-        if (begins) cut = {1, s.q0, tile * R, rows, head, owner_of(seg0 + units - 1), 0, 0};
+        if (begins && lane == 0)
+          cuts_of(a)[atomicAdd(counter_of(a, kCuts), 1u)] = {part, owner_of(seg0 + units - 1), head, s.q0, tile * R, rows, 0, 0};
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -898,7 +895,7 @@ __global__ void __launch_bounds__((WALK ? kWalkWarps : kChunkWarps) * 32,
         __syncthreads();
         if (s_last) {
           __threadfence();
-          cut = {1, s.q0, tile * R, rows, head, 0, 0, 0};
+          const Cut cut = {0, 0, head, s.q0, tile * R, rows, 0, 0};
           reinterpret_cast<Join<D, R, kThreads>*>(smem)->run(
               a, units, [&](int p) { return slot_of<D, R>(a, seg0 + p); }, cut, gv);
           if (tid == 0) counters_of(a)[seg0] = 0;
@@ -909,20 +906,27 @@ __global__ void __launch_bounds__((WALK ? kWalkWarps : kChunkWarps) * 32,
   }
 }
 
-// Joins the parts of a segment whose first part is blockIdx.x, if there is one.
+// Joins the parts of the segments that the walk has cut, a CTA each in turn.
 template <int D, int R>
 __global__ void __launch_bounds__(kAttnJoinThreads) rows_join_kernel(const AttnArgs a) {
   __shared__ Join<D, R, kAttnJoinThreads> join;
-  const int first = int(blockIdx.x);
   griddep_wait();
   griddep_launch_dependents();
-  const int parts = __ldcg(parts_of(a));
-  const int4 c0 = __ldcg(reinterpret_cast<const int4*>(cuts_of(a) + first)), c1 = __ldcg(reinterpret_cast<const int4*>(cuts_of(a) + first) + 1);
-  if (first == 0 && threadIdx.x == 0) *claims_of(a) = 0;
-  if (first >= parts || !c0.x) return;
-  const Cut cut = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, 0, 0};
-  join.run(a, cut.last - first + 1, [&](int p) { return slot_of<D, R>(a, 2 * int64_t(first + p) + (p == 0 ? 1 : 0)); }, cut,
-           __ldg(a.v_scale));
+  const int n = int(__ldcg(counter_of(a, kCuts)));
+  const float gv = __ldg(a.v_scale);
+  for (int i = int(blockIdx.x); i < n; i += int(gridDim.x)) {
+    const int4 c0 = __ldcg(reinterpret_cast<const int4*>(cuts_of(a) + i));
+    const int4 c1 = __ldcg(reinterpret_cast<const int4*>(cuts_of(a) + i) + 1);
+    const Cut cut = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, 0, 0};
+    join.run(a, cut.last - cut.first + 1,
+             [&](int p) { return slot_of<D, R>(a, 2 * int64_t(cut.first + p) + (p == 0 ? 1 : 0)); }, cut, gv);
+  }
+  // The last CTA leaves the counters at zero (its own wraps around).
+  __syncthreads();
+  if (threadIdx.x == 0 && atomicInc(counter_of(a, kDone), gridDim.x - 1) == gridDim.x - 1) {
+    *counter_of(a, kClaims) = 0;
+    *counter_of(a, kCuts) = 0;
+  }
 }
 
 }  // namespace

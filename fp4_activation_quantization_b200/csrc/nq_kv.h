@@ -85,7 +85,7 @@ struct AttnArgs {
 // describes the parts; their values follow.
 constexpr int kAttnCounterBytes = 1 << 14;
 constexpr int kAttnHeader = 1 << 19;
-constexpr int kAttnMaxParts = (kAttnHeader - kAttnCounterBytes - 64) / 32;
+constexpr int kAttnMaxParts = (kAttnHeader - kAttnCounterBytes) / 32;
 
 // Kernels (nullptr: not built).
 const void* kv_plan_kernel();
@@ -97,7 +97,7 @@ constexpr int kKvCopyThreads = 256;
 constexpr int kAttnJoinThreads = 128;
 struct AttnRows {
   const void* kernel;
-  const void* join;  // walk: a CTA per part, after it
+  const void* join;  // walk: after it
   size_t smem;
   int threads;
 };

@@ -263,7 +263,7 @@ nq_status nq_attention_nvfp4_kv(const void* q, int64_t ld_q_token, int64_t ld_q_
   if (grid <= 0) return error(NQ_ERR_CUDA, "%s: no CUDA device", fn);
   void* args[] = {&a};
   if (segments <= grid / 2) {
-    const int64_t room = (workspace_bytes - nq::kAttnHeader) / slot, counters = nq::kAttnCounterBytes / 4 - 1;
+    const int64_t room = (workspace_bytes - nq::kAttnHeader) / slot, counters = nq::kAttnCounterBytes / 4 - 3;
     grid = grid < room ? grid : room;
     grid = grid < counters ? grid : counters;
     if (segments * (atoms / 32 + 1) < grid) grid = segments * (atoms / 32 + 1);
@@ -282,7 +282,7 @@ nq_status nq_attention_nvfp4_kv(const void* q, int64_t ld_q_token, int64_t ld_q_
   nq_status s = nq::host::launch(fn, k.kernel, unsigned(grid), k.threads, k.smem, args,
                                  (flags & NQ_FLAG_PDL) != 0, static_cast<cudaStream_t>(stream));
   if (s == NQ_OK)  // may start while the first launch ends; it waits for its results
-    s = nq::host::launch(fn, k.join, unsigned(2 * grid * warps), nq::kAttnJoinThreads, 0, args, true,
+    s = nq::host::launch(fn, k.join, unsigned(4 * grid), nq::kAttnJoinThreads, 0, args, true,
                          static_cast<cudaStream_t>(stream));
   return s;
 }
