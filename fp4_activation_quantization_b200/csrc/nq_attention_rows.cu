@@ -334,7 +334,7 @@ __global__ void __launch_bounds__((WALK ? kWalkWarps : kChunkWarps) * 32,
     fixed = int(min(warps, (total + 1) >> 1));
     fixed_end = total;
     parts = fixed;
-    if (fixed == warps && total >= 20 * warps) {  // small parts of four atoms or more
+    if (fixed == warps && total >= 96 * warps) {  // small parts of 20 atoms or more: shorter ones cost more than they save
       fixed_end = total / 5 * 4;
       parts = 2 * fixed;
     }

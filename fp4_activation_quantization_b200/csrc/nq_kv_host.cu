@@ -226,7 +226,7 @@ nq_status nq_attention_nvfp4_kv(const void* q, int64_t ld_q_token, int64_t ld_q_
   if (a.err == nullptr) return error(NQ_ERR_CUDA, "%s: no CUDA device", fn);
 
   const int64_t rows = (T * a.group + B - 1) / B;  // of an average request and kv head
-  if (rows > (d == 64 ? 64 : 32)) {
+  if (rows > (d == 256 ? 16 : 32)) {
     const nq::AttnTiles k = nq::attn_tiles(d);
     if (!nq::host::allow_smem(k.kernel, k.smem))
       return error(NQ_ERR_UNSUPPORTED, "%s: %zu bytes of shared memory not available", fn, k.smem);
