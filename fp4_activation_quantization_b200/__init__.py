@@ -611,7 +611,7 @@ def nq_kv_plan(cached_lens, new_lens, block_table, free_pages, free_head, tokens
     _need(tokens >= 0, "tokens must not be negative")
     # One allocation for the int32 results.
     buf = torch.empty(2 * B + 2 + tokens, dtype=_i32, device=new_lens.device)
-    cu_q, kv_lens, head_out, positions = buf.split((B + 1, B, 1, tokens))
+    cu_q, kv_lens, head_out, positions = buf.split_with_sizes((B + 1, B, 1, tokens))
     slots = torch.empty(tokens, dtype=_i64, device=new_lens.device)
     if free_head_out is None:
         free_head_out = head_out

@@ -8,8 +8,9 @@
 //
 // Both are bound by memory: a pair of key and value elements moves 4 bytes of
 // bf16 and 1.125 bytes of cache.  A thread owns one block of the key and the
-// same block of the value (32 contiguous bf16 bytes each, one 32-byte access),
-// and a warp covers 512 / D consecutive tokens of one head, so that the 8-byte
+// same block of the value (32 contiguous bf16 bytes each, one 32-byte access) of
+// two heads, whose loads all wait for the slot once, and a warp covers 512 / D
+// consecutive tokens of a head, so that the 8-byte
 // pieces into which the atom's order cuts a value row (16 bytes hold a pair of
 // tokens, 32 bytes two pairs) leave the warp as whole 32-byte sectors when the
 // tokens are consecutive.
@@ -56,21 +57,26 @@ __device__ __forceinline__ void store16(uint16_t* p, const Raw& r) {
 
 struct Place {
   int token, head, block;
-  bool live;       // a token of the batch
-  int64_t slot;    // -1: nothing to do
-  uint8_t* atom;   // of the slot
+  bool live;         // a token of the batch
+  bool second;       // a second head, head + 1
+  int64_t slot;      // -1: nothing to do
+  uint8_t* atom;     // of the slot, first head
+  int64_t per_head;  // bytes between the heads' atoms
 };
 
-// The block that this thread owns: warps count heads fastest, then groups of
-// 512 / D tokens.
+// The blocks that this thread owns, of two heads: warps count pairs of heads
+// fastest, then groups of 512 / D tokens.
 template <int D>
 __device__ __forceinline__ Place place_of(const KvCopyArgs& a) {
   constexpr int kBlocks = D / 16, kTokens = 32 / kBlocks;
   const int64_t warp = (int64_t(blockIdx.x) * kKvCopyThreads + threadIdx.x) >> 5;
   const int lane = int(threadIdx.x) & 31;
   Place p;
-  const int64_t group = warp / a.cache.heads;
-  p.head = int(warp - group * a.cache.heads);
+  const int pairs = (a.cache.heads + 1) >> 1;
+  const int64_t group = warp / pairs;
+  p.head = 2 * int(warp - group * pairs);
+  p.second = p.head + 1 < a.cache.heads;
+  p.per_head = int64_t(18 * D) << (a.cache.log_page - 4);
   const int64_t token = group * kTokens + lane / kBlocks;
   p.block = lane % kBlocks;
   p.live = token < a.T;
@@ -84,8 +90,7 @@ __device__ __forceinline__ Place place_of(const KvCopyArgs& a) {
       p.slot = -1;
     } else {
       const int in = int(p.slot) & ((1 << a.cache.log_page) - 1);
-      const int per_head = 18 * D << (a.cache.log_page - 4);
-      p.atom = a.cache.base + page * a.cache.page_stride + int64_t(p.head) * per_head + (in >> 4) * (18 * D);
+      p.atom = a.cache.base + page * a.cache.page_stride + p.head * p.per_head + (in >> 4) * (18 * D);
     }
   }
   return p;
@@ -113,32 +118,40 @@ __device__ __forceinline__ void quantize_block(const Raw& r, float g, float ngr,
 }
 
 template <int D, bool VEC>
-__global__ void __launch_bounds__(kKvCopyThreads) append_kernel(const KvCopyArgs a) {
+__global__ void __launch_bounds__(kKvCopyThreads, 4) append_kernel(const KvCopyArgs a) {
   griddep_wait();
   const Place p = place_of<D>(a);
-  Raw k{}, v{};
-  if (p.slot >= 0) {
-    k = load16<VEC>(a.k + p.token * a.ld_kt + p.head * a.ld_kh + 16 * p.block);
-    v = load16<VEC>(a.v + p.token * a.ld_vt + p.head * a.ld_vh + 16 * p.block);
-  }
+  Raw k[2] = {}, v[2] = {};
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    if (p.slot >= 0 && (h == 0 || p.second)) {
+      k[h] = load16<VEC>(a.k + p.token * a.ld_kt + (p.head + h) * a.ld_kh + 16 * p.block);
+      v[h] = load16<VEC>(a.v + p.token * a.ld_vt + (p.head + h) * a.ld_vh + 16 * p.block);
+    }
   griddep_launch_dependents();
   const float gk = __ldg(a.k_scale), gv = __ldg(a.v_scale);
-  uint2 kc, vc;
-  uint32_t ks, vs;
-  quantize_block(k, gk, -__frcp_rn(gk), fast_div_ok(gk), &kc, &ks);
-  quantize_block(v, gv, -__frcp_rn(gv), fast_div_ok(gv), &vc, &vs);
-  if (p.slot < 0) return;
+  const float nrk = -__frcp_rn(gk), nrv = -__frcp_rn(gv);
+  const bool fast_k = fast_div_ok(gk), fast_v = fast_div_ok(gv);
   const int t = int(p.slot) & 15;
-  *reinterpret_cast<uint2*>(p.atom + KvAtom<D>::k_codes(t, p.block)) = kc;
-  uint8_t* vp = p.atom + KvAtom<D>::v_codes(t, p.block);
-  if constexpr (D == 64) {  // the block's halves belong to two lanes, 64 bytes apart
-    *reinterpret_cast<uint32_t*>(vp) = vc.x;
-    *reinterpret_cast<uint32_t*>(vp + 64) = vc.y;
-  } else {
-    *reinterpret_cast<uint2*>(vp) = vc;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint2 kc, vc;
+    uint32_t ks, vs;
+    quantize_block(k[h], gk, nrk, fast_k, &kc, &ks);
+    quantize_block(v[h], gv, nrv, fast_v, &vc, &vs);
+    if (p.slot < 0 || (h == 1 && !p.second)) continue;
+    uint8_t* atom = p.atom + h * p.per_head;
+    *reinterpret_cast<uint2*>(atom + KvAtom<D>::k_codes(t, p.block)) = kc;
+    uint8_t* vp = atom + KvAtom<D>::v_codes(t, p.block);
+    if constexpr (D == 64) {  // the block's halves belong to two lanes, 64 bytes apart
+      *reinterpret_cast<uint32_t*>(vp) = vc.x;
+      *reinterpret_cast<uint32_t*>(vp + 64) = vc.y;
+    } else {
+      *reinterpret_cast<uint2*>(vp) = vc;
+    }
+    atom[KvAtom<D>::k_scale(t, p.block)] = uint8_t(ks);
+    atom[KvAtom<D>::v_scale(t, p.block)] = uint8_t(vs);
   }
-  p.atom[KvAtom<D>::k_scale(t, p.block)] = uint8_t(ks);
-  p.atom[KvAtom<D>::v_scale(t, p.block)] = uint8_t(vs);
 }
 
 __device__ __forceinline__ Raw dequantize_block(uint2 codes, uint32_t sf, float g) {
@@ -162,25 +175,32 @@ template <int D, bool VEC>
 __global__ void __launch_bounds__(kKvCopyThreads) gather_kernel(const KvCopyArgs a) {
   griddep_wait();
   const Place p = place_of<D>(a);
-  uint2 kc = make_uint2(0u, 0u), vc = kc;
-  uint32_t ks = 0, vs = 0;
-  if (p.slot >= 0) {
-    const int t = int(p.slot) & 15;
-    kc = *reinterpret_cast<const uint2*>(p.atom + KvAtom<D>::k_codes(t, p.block));
-    const uint8_t* vp = p.atom + KvAtom<D>::v_codes(t, p.block);
-    if constexpr (D == 64)
-      vc = make_uint2(*reinterpret_cast<const uint32_t*>(vp), *reinterpret_cast<const uint32_t*>(vp + 64));
-    else
-      vc = *reinterpret_cast<const uint2*>(vp);
-    ks = p.atom[KvAtom<D>::k_scale(t, p.block)];
-    vs = p.atom[KvAtom<D>::v_scale(t, p.block)];
-  }
+  uint2 kc[2] = {}, vc[2] = {};
+  uint32_t ks[2] = {}, vs[2] = {};
+  const int t = int(p.slot) & 15;
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    if (p.slot >= 0 && (h == 0 || p.second)) {
+      const uint8_t* atom = p.atom + h * p.per_head;
+      kc[h] = *reinterpret_cast<const uint2*>(atom + KvAtom<D>::k_codes(t, p.block));
+      const uint8_t* vp = atom + KvAtom<D>::v_codes(t, p.block);
+      if constexpr (D == 64)
+        vc[h] = make_uint2(*reinterpret_cast<const uint32_t*>(vp), *reinterpret_cast<const uint32_t*>(vp + 64));
+      else
+        vc[h] = *reinterpret_cast<const uint2*>(vp);
+      ks[h] = atom[KvAtom<D>::k_scale(t, p.block)];
+      vs[h] = atom[KvAtom<D>::v_scale(t, p.block)];
+    }
   griddep_launch_dependents();
   if (!p.live) return;
   // A padding token reads as zeros whatever the global scales hold.
   const float gk = p.slot >= 0 ? __ldg(a.k_scale) : 0.0f, gv = p.slot >= 0 ? __ldg(a.v_scale) : 0.0f;
-  store16<VEC>(a.k + p.token * a.ld_kt + p.head * a.ld_kh + 16 * p.block, dequantize_block(kc, ks, gk));
-  store16<VEC>(a.v + p.token * a.ld_vt + p.head * a.ld_vh + 16 * p.block, dequantize_block(vc, vs, gv));
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    if (h == 1 && !p.second) continue;
+    store16<VEC>(a.k + p.token * a.ld_kt + (p.head + h) * a.ld_kh + 16 * p.block, dequantize_block(kc[h], ks[h], gk));
+    store16<VEC>(a.v + p.token * a.ld_vt + (p.head + h) * a.ld_vh + 16 * p.block, dequantize_block(vc[h], vs[h], gv));
+  }
 }
 
 }  // namespace

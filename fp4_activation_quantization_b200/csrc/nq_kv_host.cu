@@ -78,7 +78,7 @@ nq_status kv_copy(const char* fn, bool gather, const void* k, int64_t ld_kt, int
   a.T = int32_t(T);
   const bool vec = aligned(k, 32) && aligned(v, 32) && (ld_kt | ld_vt) % 16 == 0 && (heads == 1 || (ld_kh | ld_vh) % 16 == 0);
   const int per_warp = 512 / d;  // tokens of a warp
-  const int64_t warps = (T + per_warp - 1) / per_warp * heads;
+  const int64_t warps = (T + per_warp - 1) / per_warp * ((heads + 1) / 2);  // two heads a warp
   const int64_t grid = (warps + nq::kKvCopyThreads / 32 - 1) / (nq::kKvCopyThreads / 32);
   if (grid > kInt32Max) return error(NQ_ERR_UNSUPPORTED, "%s: too many tokens", fn);
   a.err = nq::host::error_word();
