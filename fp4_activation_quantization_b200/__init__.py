@@ -153,7 +153,8 @@ def nq_selftest_division(divisors, a_bits_begin: int = 0, count: int = 1 << 32, 
 
 def nq_check_device_errors() -> None:
     """Raise NQError if a kernel recorded an error since the last check (a MoE
-    destination row out of range).  Synchronous: waits for every stream of the
+    destination row out of range; a key/value slot or page out of range, a plan
+    that ran out of pages).  Synchronous: waits for every stream of the
     current device, then reads and clears the device error word atomically."""
     _check(_get_lib().nq_check_device_errors(), "nq_check_device_errors")
 
@@ -740,8 +741,11 @@ def nq_attention_nvfp4_kv(q, cache, block_table, kv_lens, cu_q, k_scale, v_scale
         ld_lse, s1 = lse.stride()
         _need(heads <= 1 or s1 == 1, "lse must have a contiguous last dimension")
         lse_p, ld_lse = lse.data_ptr(), (ld_lse if T > 1 else max(ld_lse, heads))
+    _need(0 <= window < 1 << 31, "window must lie in 0 .. 2^31 - 1")
     if workspace is None:
-        workspace = torch.zeros(ATTENTION_WORKSPACE_BYTES, dtype=_u8, device=q.device)
+        on = stream if stream is None or isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(stream, q.device)
+        with torch.cuda.stream(on):  # zeroed, and given back, in the order of the stream that the call runs on
+            workspace = torch.zeros(ATTENTION_WORKSPACE_BYTES, dtype=_u8, device=q.device)
     elif _device_of(workspace) != dev or workspace.dtype is not _u8 or workspace.dim() != 1 or not workspace.is_contiguous():
         _wrong(dev, workspace=(workspace, _u8, (None,), True))
     _launch(dev, "nq_attention_nvfp4_kv",

@@ -743,15 +743,14 @@ __global__ void __launch_bounds__((WALK ? kWalkWarps : kChunkWarps) * 32,
     // Atoms [i_lo, i_hi) are seen whole by every row.
     const int i_lo = lo_full > t0 ? (lo_full - t0 + 15) >> 4 : 0;
     const int i_hi = hi_full > t0 ? min(n_atoms, (hi_full - t0) >> 4) : 0;
+    bool lost = false;
 #pragma unroll 1
     for (int i = 0; i < n_atoms; i += 2) {
       __syncwarp();  // all lanes have read the pair before
       issue_pair();
       const uint8_t* atom = ring_p + rd_slot * (2 * kAtom);
-      if (!mbar_wait(bars + 8 * rd_slot, rd_parity)) {
-        // Never in a sound run: the results of this call are not valid.
-        if (lane == 0) atomicOr(a.err, kErrWait);
-      }
+      lost = __any_sync(kFull, !mbar_wait(bars + 8 * rd_slot, rd_parity));
+      if (lost) break;
       if (++rd_slot == kStages) rd_slot = 0, rd_parity ^= 1;
       const uint32_t absent = (missing >> (2 * kStages - 2)) & 3u;  // bit 1: the first atom
       if (i >= i_lo && i + 2 <= i_hi && absent == 0) {
@@ -786,6 +785,17 @@ __global__ void __launch_bounds__((WALK ? kWalkWarps : kChunkWarps) * 32,
       }
     }
     __syncwarp();
+    if (lost) {
+      // Never in a sound run: the results of this call are not valid.  Waits, as long, for the copies behind the one
+      // that did not come, and takes no further part.
+      if (lane == 0) atomicOr(a.err, kErrWait);
+      if (++rd_slot == kStages) rd_slot = 0, rd_parity ^= 1;
+      while (rd_slot != wr_slot) {
+        mbar_wait(bars + 8 * rd_slot, rd_parity);
+        if (++rd_slot == kStages) rd_slot = 0, rd_parity ^= 1;
+      }
+      if constexpr (WALK) return;
+    }
 
     // ---- the segment's end: sums over the lanes of a column
 #pragma unroll

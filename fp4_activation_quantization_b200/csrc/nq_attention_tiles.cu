@@ -681,8 +681,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
     // ----------------------------------------------------------- products ----
     regs_dec<C::kRegsMma>();
     if (warp == 12 && n > 0) {
-      // A warp for each tile (on schedulers of their own), so that neither tile's
-      // hand-overs wait behind the other's.  The whole warp walks the loop, so that descriptors and counters stay in
+      // The whole warp walks the loop, so that descriptors and counters stay in
       // uniform registers; one elected lane issues.  Rolled loops: this code runs
       // for a moment between long waits, and unrolled it was slowed to 100 cycles
       // per product by instruction fetches (a prompt of 8192: 757 us).

@@ -99,13 +99,15 @@ __global__ void __launch_bounds__(kKvPlanThreads) plan_kernel(const KvPlanArgs a
         first_token[b] = int32_t(min(uint32_t(before >> 32), uint32_t(a.T)));
         first_page[b] = int32_t(uint32_t(before));
       }
-      before += item[i];
+      const uint64_t after = before + item[i];
+      bad |= after < before || uint32_t(after) < uint32_t(before);  // more than 2^32 tokens or pages
+      before = after;
     }
     carry = all;
   }
   const uint32_t tokens = uint32_t(carry >> 32);
   const int32_t pages = int32_t(uint32_t(carry));
-  if (tokens > uint32_t(a.T) || int64_t(head) + pages > a.n_free) bad = true;
+  if (tokens > uint32_t(a.T) || int64_t(head) + uint32_t(pages) > a.n_free) bad = true;
   if (tid == 0) {
     first_token[a.B] = int32_t(min(tokens, uint32_t(a.T)));
     first_page[a.B] = pages;
@@ -133,7 +135,8 @@ __global__ void __launch_bounds__(kKvPlanThreads) plan_kernel(const KvPlanArgs a
   }
   for (int f = me; f < pages; f += step) {
     const int b = last_not_above(first_page, a.B, f);
-    a.table[b * a.ld_table + held(b) + (f - first_page[b])] = fresh(f);
+    const int64_t column = int64_t(held(b)) + f - first_page[b];
+    if (column < a.width) a.table[b * a.ld_table + column] = fresh(f);  // always, unless the sums ran over
   }
   const int32_t mask = (1 << a.log_page) - 1;
   for (int t = me; t < a.T; t += step) {

@@ -474,6 +474,80 @@ def test_other_stream_and_programmatic_launch(nq):
     assert all(torch.equal(o, want) for o in outs)
 
 
+def many(nq, B, heads, kv_heads, D, least, most, seed, rows=1):
+    """B requests of `rows` tokens whose pages are the same (a shared prefix), of lengths least ... most."""
+    s = make(nq, [rows], [most], heads, kv_heads, D, 16, seed=seed)
+    gen = torch.Generator("cuda").manual_seed(seed)
+    t = torch.randint(least, most + 1, (B,), generator=gen, device="cuda").tolist()
+    n = [rows] * B
+    s.update(q=torch.randn((B * rows, heads, D), generator=gen, device="cuda").bfloat16(), table=s["table"].repeat(B, 1),
+             kv_lens=i32(t), cu=i32(np.arange(B + 1) * rows), n=n, t=t)
+    return s
+
+
+# Lengths from one tile of keys to shares that are long enough to be claimed in small parts (64 x 8 heads x 7500).
+@pytest.mark.parametrize("B,heads,kv_heads,D,least,most,rows", [
+    (400, 8, 2, 128, 1, 300, 1), (64, 8, 8, 64, 7000, 8000, 1), (200, 16, 4, 64, 5, 2000, 3), (200, 8, 4, 256, 5, 900, 1),
+    (150, 16, 4, 128, 4, 1200, 3)])
+def test_many_requests_share_out_evenly(nq, B, heads, kv_heads, D, least, most, rows):
+    s = many(nq, B, heads, kv_heads, D, least, most, seed=15, rows=rows)
+    ws = torch.zeros(nq.ATTENTION_WORKSPACE_BYTES, dtype=torch.uint8, device="cuda")
+    out, lse = check(nq, s, workspace=ws)
+    for _ in range(3):  # the parts that are claimed differ from run to run, the bits do not
+        again, lse_again = check(nq, s, workspace=ws)
+        assert torch.equal(again, out) and torch.equal(lse_again, lse)
+
+
+def test_many_requests_captured_with_a_shared_workspace(nq):
+    s = many(nq, 400, 8, 2, 128, 1, 500, seed=16)
+    ws = torch.zeros(nq.ATTENTION_WORKSPACE_BYTES, dtype=torch.uint8, device="cuda")
+    out, other = torch.empty_like(s["q"]), torch.empty_like(s["q"])
+    lens = s["kv_lens"].clone()
+    args = (s["cache"], s["table"], lens, s["cu"], s["gk"], s["gv"])
+    graphs = []
+    stream = torch.cuda.Stream()
+    for o in (out, other):
+        g = torch.cuda.CUDAGraph()
+        stream.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.graph(g, stream=stream):
+            for _ in range(2):  # the second call may start under the first one's end
+                nq.nq_attention_nvfp4_kv(s["q"], *args, out=o, workspace=ws, flags=nq.FLAG_PDL)
+        graphs.append(g)
+    for cut in (0, 100, 499):
+        lens.copy_((s["kv_lens"] - cut).clamp_(min=0))
+        for g in graphs:
+            g.replay()
+        want, _ = nq.nq_attention_nvfp4_kv(s["q"], *args)
+        assert torch.equal(out, want) and torch.equal(other, want)
+    nq.nq_check_device_errors()
+
+
+def test_own_workspace_on_another_stream(nq):
+    """Without a workspace the call zeroes one in the order of its stream, whatever the memory held."""
+    s = many(nq, 400, 8, 2, 128, 1, 500, seed=17)
+    args = (s["cache"], s["table"], s["kv_lens"], s["cu"], s["gk"], s["gv"])
+    want, _ = nq.nq_attention_nvfp4_kv(s["q"], *args)
+    torch.cuda.synchronize()
+    stream = torch.cuda.Stream()
+    for handle in (stream, stream.cuda_stream):
+        out = torch.empty_like(want)
+        torch.cuda.synchronize()
+        nq.nq_attention_nvfp4_kv(s["q"], *args, out=out, stream=handle)
+        stream.synchronize()
+        assert torch.equal(out, want)
+
+
+def test_plan_reports_sums_past_32_bits(nq):
+    """Four requests of 2^30 tokens: their sum is 0 modulo 2^32."""
+    B, width = 4, (1 << 30) // 128
+    table = torch.full((B, width + 1), -7, dtype=torch.int32, device="cuda")
+    zero = i32([0] * B)
+    cu, kv, pos, slots, _ = nq.nq_kv_plan(zero, i32([1 << 30] * B), table[:, :width], i32([5, 6]), i32([0]), 8, 128)
+    with pytest.raises(nq.NQError, match="bit 3"):
+        nq.nq_check_device_errors()
+    assert bool((table[:, width] == -7).all()) and kv.tolist() == [1 << 30] * B
+
+
 def test_binding_refusals(nq):
     s = make(nq, [1], [20], 4, 2, 128, 16)
     good = dict(q=s["q"], cache=s["cache"], block_table=s["table"], kv_lens=s["kv_lens"], cu_q=s["cu"], k_scale=s["gk"],
@@ -490,6 +564,9 @@ def test_binding_refusals(nq):
         nq.nq_attention_nvfp4_kv(**good, lse=torch.empty(1, 3, device="cuda"))
     with pytest.raises(nq.NQError):
         nq.nq_attention_nvfp4_kv(**good, workspace=torch.zeros(1 << 20, dtype=torch.uint8, device="cuda"))
+    for window in (-1, 1 << 32):
+        with pytest.raises(ValueError, match="window"):
+            nq.nq_attention_nvfp4_kv(**good, window=window)
     with pytest.raises(ValueError):
         nq.nq_kv_append_nvfp4(s["q"], s["q"], torch.zeros(1, dtype=torch.int64, device="cuda"), s["cache"], s["gk"], s["gv"])
     with pytest.raises(ValueError):
