@@ -225,58 +225,70 @@ nq_status nq_attention_nvfp4_kv(const void* q, int64_t ld_q_token, int64_t ld_q_
   a.err = nq::host::error_word();
   if (a.err == nullptr) return error(NQ_ERR_CUDA, "%s: no CUDA device", fn);
 
-  const int64_t rows = (T * a.group + B - 1) / B;  // of an average request and kv head
-  if (rows > (d == 256 ? 16 : 32)) {
-    const nq::AttnTiles k = nq::attn_tiles(d);
-    if (!nq::host::allow_smem(k.kernel, k.smem))
-      return error(NQ_ERR_UNSUPPORTED, "%s: %zu bytes of shared memory not available", fn, k.smem);
-    const int64_t tiles = T * a.group / k.rows + B, items = tiles * kv_heads;
-    const int64_t sms = nq::host::resident_ctas(k.kernel, nq::kAttnTilesThreads, k.smem);
-    if (sms <= 0) return error(NQ_ERR_CUDA, "%s: no CUDA device", fn);
-    const int64_t room = (workspace_bytes - nq::kAttnHeader) / (int64_t(k.rows) * (d + 2) * int64_t(sizeof(float)));
-    int64_t splits = (sms < room ? sms : room) / items;
-    const int64_t blocks = (int64_t(table_width) * page_size + 511) / 512;  // at least four blocks of keys each
-    splits = splits < blocks ? splits : blocks;
-    splits = splits < 1 ? 1 : splits;
-    const int64_t grid = items * splits, join_grid = items * (k.rows / 8);
-    if (grid > kInt32Max || join_grid > kInt32Max) return error(NQ_ERR_UNSUPPORTED, "%s: T or B too large", fn);
-    a.tiles = int32_t(tiles);
-    a.splits = int32_t(splits);
-    void* args[] = {&a};
-    nq_status s = nq::host::launch(fn, k.kernel, unsigned(grid), nq::kAttnTilesThreads, k.smem, args,
-                                   (flags & NQ_FLAG_PDL) != 0, static_cast<cudaStream_t>(stream));
-    if (s == NQ_OK && splits > 1)
-      s = nq::host::launch(fn, k.join, unsigned(join_grid), 256, 0, args, (flags & NQ_FLAG_PDL) != 0,
-                           static_cast<cudaStream_t>(stream));
-    return s;
-  }
-  const int n_tiles = rows <= 8 ? 1 : (rows <= 16 || d > 64 ? 2 : 4);
-  // Fewer segments (request, row tile, kv head) than half the CTAs that the GPU holds: a chunk a CTA and one
+  // Rows of an average request and kv head: few of them go to the rows kernel,
+  // in 8-row tiles of which a warp takes n_tiles.  Segments (request, row tile, kv
+  // head) fewer than half the CTAs that the GPU holds: a chunk a CTA and one
   // launch; else a share a warp and a second launch.
-  const int64_t segments = (T * a.group / (8 * n_tiles) + B) * kv_heads;
-  const int64_t slot = int64_t(8 * n_tiles) * (d + 2) * int64_t(sizeof(float));
-  const int64_t atoms = (int64_t(table_width) * page_size + 15) / 16;
+  const int64_t rows = (T * a.group + B - 1) / B;
+  const int n_tiles = rows <= 8 ? 1 : (d > 64 || rows <= 16 || (rows > 32 && rows <= 48) ? 2 : 4);
   nq::AttnRows k = nq::attn_rows(d, n_tiles, false);
   if (!nq::host::allow_smem(k.kernel, k.smem))
     return error(NQ_ERR_UNSUPPORTED, "%s: %zu bytes of shared memory not available", fn, k.smem);
   int64_t grid = nq::host::resident_ctas(k.kernel, k.threads, k.smem);
   if (grid <= 0) return error(NQ_ERR_CUDA, "%s: no CUDA device", fn);
+  const int64_t segments = (T * a.group / (8 * n_tiles) + B) * kv_heads;
+  const bool few = segments <= grid / 2;
+  // Rows kernel / 128-row tiles, 8 kv heads, us:
+  //                             d = 64           d = 128                        d = 256
+  //   24 requests of 4096 keys  64 rows  83/116  48 rows 122/135, 64 rows 149/135  24 rows 150/182, 32 rows 191/184
+  //   200 requests of 700 keys  64 rows 144/203  48 rows 173/270, 64 rows 220/277  24 rows 212/371, 32 rows 273/387
+  //   2 requests of 8192 (few)  32 rows  24/31   32 rows  28/39,  48 rows  37/41   24 rows  45/51,  32 rows  45/51
+  //   1 request of 65536 (few)  32 rows  39/64   32 rows  61/78,  48 rows  86/78   16 rows  66/100, 24 rows 111/100
+  const int64_t most = d == 256 ? 24 : (few ? 32 : (d == 128 ? 48 : 64));
+  if (rows > most) {
+    const nq::AttnTiles t = nq::attn_tiles(d);
+    if (!nq::host::allow_smem(t.kernel, t.smem))
+      return error(NQ_ERR_UNSUPPORTED, "%s: %zu bytes of shared memory not available", fn, t.smem);
+    const int64_t tiles = T * a.group / t.rows + B, items = tiles * kv_heads;
+    const int64_t sms = nq::host::resident_ctas(t.kernel, nq::kAttnTilesThreads, t.smem);
+    if (sms <= 0) return error(NQ_ERR_CUDA, "%s: no CUDA device", fn);
+    const int64_t room = (workspace_bytes - nq::kAttnHeader) / (int64_t(t.rows) * (d + 2) * int64_t(sizeof(float)));
+    int64_t splits = (sms < room ? sms : room) / items;
+    const int64_t blocks = (int64_t(table_width) * page_size + 511) / 512;  // at least four blocks of keys each
+    splits = splits < blocks ? splits : blocks;
+    splits = splits < 1 ? 1 : splits;
+    const int64_t ctas = items * splits, join_grid = items * (t.rows / 8);
+    if (ctas > kInt32Max || join_grid > kInt32Max) return error(NQ_ERR_UNSUPPORTED, "%s: T or B too large", fn);
+    a.tiles = int32_t(tiles);
+    a.splits = int32_t(splits);
+    void* args[] = {&a};
+    nq_status s = nq::host::launch(fn, t.kernel, unsigned(ctas), nq::kAttnTilesThreads, t.smem, args,
+                                   (flags & NQ_FLAG_PDL) != 0, static_cast<cudaStream_t>(stream));
+    if (s == NQ_OK && splits > 1)
+      s = nq::host::launch(fn, t.join, unsigned(join_grid), 256, 0, args, (flags & NQ_FLAG_PDL) != 0,
+                           static_cast<cudaStream_t>(stream));
+    return s;
+  }
+  const int64_t atoms = (int64_t(table_width) * page_size + 15) / 16;
+  const auto slot = [&](int tiles) { return int64_t(8 * tiles) * (d + 2) * int64_t(sizeof(float)); };
   void* args[] = {&a};
-  if (segments <= grid / 2) {
-    const int64_t room = (workspace_bytes - nq::kAttnHeader) / slot, counters = nq::kAttnCounterBytes / 4 - 3;
+  if (few) {
+    const int64_t room = (workspace_bytes - nq::kAttnHeader) / slot(n_tiles), counters = nq::kAttnCounterBytes / 4 - 3;
     grid = grid < room ? grid : room;
     grid = grid < counters ? grid : counters;
     if (segments * (atoms / 32 + 1) < grid) grid = segments * (atoms / 32 + 1);
     return nq::host::launch(fn, k.kernel, unsigned(grid), k.threads, k.smem, args, (flags & NQ_FLAG_PDL) != 0,
                             static_cast<cudaStream_t>(stream));
   }
-  k = nq::attn_rows(d, n_tiles, true);
+  // 256 x 16 rows do not fit a thread's registers beside the walk (24 requests: 108 us, twice 8 rows 103).
+  const int walk_tiles = d == 256 ? 1 : n_tiles;
+  k = nq::attn_rows(d, walk_tiles, true);
   if (!nq::host::allow_smem(k.kernel, k.smem))
     return error(NQ_ERR_UNSUPPORTED, "%s: %zu bytes of shared memory not available", fn, k.smem);
   grid = nq::host::resident_ctas(k.kernel, k.threads, k.smem);
   const int warps = k.threads / 32;
   if (grid <= 0) return error(NQ_ERR_CUDA, "%s: no CUDA device", fn);
-  int64_t room = (workspace_bytes - nq::kAttnHeader) / (2 * slot) / 2;  // two parts a warp, two slots each
+  int64_t room = (workspace_bytes - nq::kAttnHeader) / (2 * slot(walk_tiles)) / 2;  // two parts a warp, two slots each
   room = room < nq::kAttnMaxParts / 2 ? room : nq::kAttnMaxParts / 2;
   grid = grid < room / warps ? grid : room / warps;
   nq_status s = nq::host::launch(fn, k.kernel, unsigned(grid), k.threads, k.smem, args,
