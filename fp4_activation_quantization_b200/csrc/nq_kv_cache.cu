@@ -10,10 +10,11 @@
 // bf16 and 1.125 bytes of cache.  A thread owns one block of the key and the
 // same block of the value (32 contiguous bf16 bytes each, one 32-byte access) of
 // two heads, whose loads all wait for the slot once, and a warp covers 512 / D
-// consecutive tokens of a head, so that the 8-byte
-// pieces into which the atom's order cuts a value row (16 bytes hold a pair of
-// tokens, 32 bytes two pairs) leave the warp as whole 32-byte sectors when the
-// tokens are consecutive.
+// consecutive tokens of a head, so that the 8-byte pieces into which the atom's
+// order cuts a value row (16 bytes hold a pair of tokens, 32 bytes two pairs) leave
+// the warp as whole 32-byte sectors when the tokens are consecutive.
+// 65536 tokens, 8 heads of 128: append 60.4 us (5.7 TB/s; 69 with one head a
+// thread), gather 55 us (6.2 TB/s, 0.95 of copy bandwidth; 64).
 #include "nq_kv_layout.cuh"
 #include "nq_row_kernel.cuh"
 
