@@ -5,8 +5,8 @@
 // exact in f16, query rows scaled by a power of two, float32 accumulation, f16
 // weights, the running maximum raised only by more than 2^8.
 //
-// One CTA owns NS tiles of 128 (token, head of the group) rows of one request
-// and kv head and walks its keys in blocks of 128:
+// One CTA an SM takes items in turn: NS tiles of 128 (token, head of the group)
+// rows of one request and kv head.  It walks an item's keys in blocks of 128:
 //   producer warps   4-bit atoms -> f16 K or V block in shared memory (128-byte
 //                    rows, 128-byte swizzle; the next item's bytes are already
 //                    in registers while one is converted);
@@ -19,6 +19,14 @@
 // under the other's products.  D = 256: O alone takes 256 of the 512 tensor
 // memory columns, so one tile with two S buffers, the next block's S being
 // computed under this block's exponentials.
+//
+// A warp finds the next item while this one is worked on, the producers go on to
+// its keys while the last blocks are multiplied, and the barriers count on, so that
+// between items only the output and the queries stand still.  (A CTA per item paid
+// about 10 us at each end: 16 chunks of 512 behind 1536 tokens, heads of 128 332 us,
+// now 317; of 256 385, now 356; of 64 506, now 461.)  Items are claimed when five
+// blocks of the item before are left: earlier, the last items went to CTAs that
+// were not the first to be free (252 us instead of 172 for 256 items).
 //
 // Every wait on an mbarrier is bounded; a CTA whose wait runs out records it in
 // the device error word, frees its tensor memory and leaves.
@@ -47,8 +55,8 @@ struct Cfg {
   static constexpr int kSmem = 131072 + kTiles * kQBytes + 1024;  // 1024: alignment
   // Registers of a thread after the split; the launch holds 512 x 128, so a
   // role above 128 asks for more and one below 128 gives some up.
-  static constexpr int kRegsSoftmax = D == 256 ? 216 : 184;
-  static constexpr int kRegsProducer = D == 256 ? 128 : 104;
+  static constexpr int kRegsSoftmax = D == 256 ? 224 : 184;
+  static constexpr int kRegsProducer = D == 256 ? 128 : 112;
   static constexpr int kRegsMma = 32;
   static_assert(kRegsSoftmax > 128 && kRegsProducer <= 128 && kRegsMma < 128, "direction of the split");
   static_assert(kTiles * kRegsSoftmax + (3 - kTiles) * kRegsProducer + kRegsMma <= 4 * 128, "register split");
@@ -71,18 +79,22 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 // Waits for the phase of the given parity to complete; false when the limit
-// runs out (no wait of a sound run comes near it) or another role gave up.
+// runs out (no wait of a sound run comes near it) or another role gave up.  NAP:
+// a wait that may take as long as an item, so it leaves the issue slots to others.
+template <bool NAP>
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* gave_up) {
   for (int i = 0; i < (1 << 22); ++i) {
     if (mbar_try(bar, parity)) return true;
     if ((i & 1023) == 1023 && *gave_up) return false;
+    if (NAP && i > 8) __nanosleep(200);
   }
   *gave_up = 1;
   return false;
 }
 // The same for a whole warp, which stays together.
+template <bool NAP = false>
 __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, volatile int* gave_up) {
-  return __all_sync(kFull, mbar_wait(bar, parity, gave_up));
+  return __all_sync(kFull, mbar_wait<NAP>(bar, parity, gave_up));
 }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -152,45 +164,50 @@ constexpr uint32_t instruction(int n, bool b_across) {
   return (1u << 4) | (b_across ? 1u << 16 : 0u) | (uint32_t(n / 8) << 17) | (uint32_t(128 / 16) << 24);
 }
 
-// The CTA's share of the batch.
+// A piece of work: up to kRows rows of a request and kv head, and a part of their keys.
 struct Item {
   int b, head, row0;  // request, kv head, first row (token * group + head of the group)
-  int rows;           // rows of the CTA, 0: nothing to do
+  int rows;           // rows, 0: none
   int q0, q_len, kv_len;
   int first, blocks;  // first key (a multiple of 16), blocks of this split
   int index, split;   // number of the item among tiles and heads, of the split
 };
 
 __device__ __forceinline__ float* partials_of(const AttnArgs& a) { return reinterpret_cast<float*>(a.workspace + kAttnHeader); }
+// Of the workspace's counters, zero between calls: items claimed beyond each CTA's first, CTAs that are done.
+__device__ __forceinline__ uint32_t* claims_of(const AttnArgs& a) {
+  return reinterpret_cast<uint32_t*>(a.workspace + kAttnCounterBytes) - 1;
+}
+__device__ __forceinline__ uint32_t* done_of(const AttnArgs& a) { return claims_of(a) - 1; }
 
+// Tiles of request b are numbered from floor(cu_q[b] * group / R) + b on: as
+// many numbers as it has tiles at least, without a sum over the requests.
 template <int R>
 __device__ __forceinline__ int64_t tile_start(const AttnArgs& a, int b, int c0) {
   return int64_t(c0) * a.group / R + b;
 }
 __device__ __forceinline__ int first_row_of(const AttnArgs& a, int b) { return min(max(a.cu_q[b], 0), a.T); }
 
-// Tiles of request b are numbered from floor(cu_q[b] * group / R) + b on: as
-// many numbers as it has tiles at least, without a sum over the requests.
-// Every thread of the CTA calls this; later tiles of a request, which see more
+// Item number `block`, by a whole warp; later tiles of a request, which see more
 // keys, come first.
 template <int R>
-__device__ __forceinline__ Item find_item(const AttnArgs& a, int block, int tiles, int threads, int* found) {
-  const int tid = int(threadIdx.x);
+__device__ __forceinline__ Item find_item(const AttnArgs& a, int block, int lane) {
   const int heads = a.cache.heads;
   Item it{};
   it.index = block / a.splits;
   it.split = block - it.index * a.splits;
-  const int tg = tiles - 1 - it.index / heads;
+  const int tg = a.tiles - 1 - it.index / heads;
   it.head = it.index % heads;
-  if (tid == 0) *found = -1;
-  __syncthreads();
-  for (int b = tid; b < a.B; b += threads) {
-    const int64_t s0 = tile_start<R>(a, b, first_row_of(a, b));
-    if (s0 <= tg && (b + 1 == a.B || tg < tile_start<R>(a, b + 1, first_row_of(a, b + 1)))) *found = b;
-  }
-  __syncthreads();
-  if (*found < 0) return it;
-  it.b = *found;
+  // The last request that starts at tg or before, 32 places at a time.
+  int from_b = 0, to_b = a.B;
+  do {
+    const int step = (to_b - from_b + 31) / 32, at = from_b + lane * step;
+    const uint32_t reached = __ballot_sync(kFull, at < to_b && tile_start<R>(a, at, first_row_of(a, at)) <= tg);
+    if (reached == 0) return it;
+    from_b += (31 - __clz(int(reached))) * step;
+    to_b = min(to_b, from_b + step);
+  } while (to_b - from_b > 1);
+  it.b = from_b;
   const int c0 = first_row_of(a, it.b), c1 = min(max(a.cu_q[it.b + 1], c0), a.T);
   it.q0 = c0;
   it.q_len = c1 - c0;
@@ -199,7 +216,7 @@ __device__ __forceinline__ Item find_item(const AttnArgs& a, int block, int tile
   it.row0 = int(row0);
   it.rows = int(min(int64_t(R), all - row0));
   it.kv_len = int(min(int64_t(max(a.kv_lens[it.b], 0)), int64_t(a.width) << a.cache.log_page));
-  // Keys that some row of the CTA sees.
+  // Keys that some row of the item sees.
   const int64_t pos0 = int64_t(it.kv_len) - it.q_len + it.row0 / a.group;
   const int64_t pos1 = int64_t(it.kv_len) - it.q_len + (it.row0 + it.rows - 1) / a.group;
   const int lo = a.window > 0 ? int(max(int64_t(0), pos0 + 1 - a.window)) & ~15 : 0;
@@ -329,21 +346,27 @@ template <int D>
 __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
   using C = Cfg<D>;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t s_bar[28];
+  __shared__ __align__(8) uint64_t s_bar[33];
   __shared__ uint32_t s_tmem, s_bad[kBad];
-  __shared__ int s_found, s_gave_up;
+  __shared__ int s_gave_up;
+  __shared__ Item s_item[2];  // this item and the next
 
   const int tid = int(threadIdx.x), warp = tid >> 5, lane = tid & 31;
   const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t ring = smem, qs = smem + 131072;
   const uint32_t bars = smem_u32(s_bar);
+  // All of these count on through the CTA's items.
   auto full = [&](int s) { return bars + 8 * s; };          // a slot holds its block
   auto empty = [&](int s) { return bars + 64 + 8 * s; };    // products that read a slot are done
   auto s_full = [&](int t) { return bars + 128 + 8 * t; };  // S of a tile (or buffer)
   auto p_full = [&](int t, int half) { return bars + 144 + 16 * t + 8 * half; };  // 64 keys of P of a tile (or buffer)
-  const uint32_t q_full = bars + 176, o_done = bars + 184;
+  auto q_full = [&](int t) { return bars + 176 + 8 * t; };   // Q of a tile
   auto o_last = [&](int t) { return bars + 192 + 8 * t; };   // the last P V of a tile
-  auto drained = [&](int t) { return bars + 208 + 8 * t; };  // after a wait ran out
+  auto item_full = [&](int s) { return bars + 208 + 8 * s; };
+  auto item_empty = [&](int s) { return bars + 224 + 8 * s; };
+  const uint32_t o_done = bars + 240;
+  const uint32_t drained = bars + 248;  // after a wait ran out
+  const uint32_t item_due = bars + 256;  // the producers are near an item's end
 
   if (tid == 0) {
     for (int s = 0; s < 8; ++s) {
@@ -354,224 +377,240 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
       mbar_init(s_full(t), 1);
       mbar_init(p_full(t, 0), 4);
       mbar_init(p_full(t, 1), 4);
-    }
-    mbar_init(q_full, 4 * C::kTiles);
-    mbar_init(o_done, 1);
-    for (int t = 0; t < 2; ++t) {
+      mbar_init(q_full(t), 4);
       mbar_init(o_last(t), 1);
-      mbar_init(drained(t), 1);
+      mbar_init(item_full(t), 1);
+      mbar_init(item_empty(t), 13);  // every warp that takes items
     }
+    mbar_init(o_done, 1);
+    mbar_init(drained, 1);
+    mbar_init(item_due, 1);
     s_gave_up = 0;
     for (int i = 0; i < kBad; ++i) s_bad[i] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  griddep_wait();
-  griddep_launch_dependents();
-  const Item it = find_item<C::kRows>(a, int(blockIdx.x), a.tiles, kThreads, &s_found);
-  if (it.rows == 0) return;
   if (warp == 12) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&s_tmem)) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     fence_before();
   }
+  griddep_wait();
+  griddep_launch_dependents();
   __syncthreads();
   fence_after();
   const uint32_t tmem = s_tmem;
   volatile int* gave_up = &s_gave_up;
-  const int tiles = it.rows > 128 ? 2 : 1;  // of this CTA
-  const int n = it.blocks;
+  // Waits for the CTA's k-th item; false: there is none.
+  auto take = [&](int k) { return mbar_wait_warp<true>(item_full(k & 1), (k >> 1) & 1, gave_up) && s_item[k & 1].rows > 0; };
+  auto leave = [&](int k) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(item_empty(k & 1));
+  };
 
   if (warp < 4 * C::kTiles) {
     // ------------------------------------------------------------ softmax ----
     regs_inc<C::kRegsSoftmax>();
-    const int t = warp >> 2, row = tid;  // row of the CTA; tile t's thread holds lane row % 128
+    const int t = warp >> 2, row = tid;  // row of the item; tile t's thread holds lane row % 128
     const uint32_t lanes = uint32_t(warp & 3) << 21;  // tensor memory: lane in the upper half
-    const bool live = row < it.rows;
-    const int x = it.row0 + row, token = x / a.group, g = x - token * a.group;
-    const int head = it.head * a.group + g;
-    float c;
-    {
-      // The row, scaled by a power of two (and the score factor's sign), as f16.
-      const uint16_t* qp = a.q + int64_t(it.q0 + token) * a.ld_qt + int64_t(head) * a.ld_qh;
-      const bool vec = (reinterpret_cast<uintptr_t>(qp) & 15) == 0;
-      auto load8 = [&](int i) {
-        if (!live) return make_uint4(0u, 0u, 0u, 0u);
-        if (vec) return __ldg(reinterpret_cast<const uint4*>(qp) + i);
-        uint32_t w[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) w[e] = uint32_t(qp[8 * i + 2 * e]) | (uint32_t(qp[8 * i + 2 * e + 1]) << 16);
-        return make_uint4(w[0], w[1], w[2], w[3]);
-      };
-      float amax = 0.0f;
-#pragma unroll 4
-      for (int i = 0; i < D / 8; ++i) {
-        float v[8];
-        unpack_bf16x8(load8(i), v);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(v[e]));
-      }
-      const float factor = a.scale_log2 * __ldg(a.k_scale);
-      const int e = int(__float_as_uint(amax) >> 23) - 127;
-      const int k = (amax == 0.0f || e > 127) ? 0 : min(14 - e, 100);
-      const float up = copysignf(__uint_as_float(uint32_t(k + 127) << 23), factor);
-      // At least the smallest normal number: 0 would make NaN of a masked key's -inf.
-      c = fmaxf(fabsf(factor) * __uint_as_float(uint32_t(127 - k) << 23), 1.17549435e-38f);
-      const uint32_t q_row = qs + t * C::kQBytes + (row & 127) * 128;
-#pragma unroll 4
-      for (int i = 0; i < D / 8; ++i) {
-        float v[8];
-        unpack_bf16x8(load8(i), v);
-        uint32_t h[4];
-#pragma unroll
-        for (int e2 = 0; e2 < 4; ++e2) h[e2] = pack_f16x2(v[2 * e2] * up, v[2 * e2 + 1] * up);
-        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(q_row + (i >> 3) * 16384 + (((i & 7) ^ (row & 7)) << 4)),
-                     "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3])
-                     : "memory");
-      }
-      fence_smem_to_mma();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(q_full);
-    }
-    int lo = 0, hi = 0;  // keys in sight, relative to the first block
-    if (live) {
-      const int64_t pos = int64_t(it.kv_len) - it.q_len + token;
-      hi = (a.causal ? int(min(int64_t(it.kv_len), max(int64_t(0), pos + 1))) : it.kv_len) - it.first;
-      lo = (a.window > 0 ? int(max(int64_t(0), pos + 1 - a.window)) : 0) - it.first;
-    }
-    // Blocks that every row of the warp sees whole need no mask.
-    int lo_all = live ? lo : -0x7fffffff, hi_all = live ? hi : 0x7fffffff;
-#pragma unroll
-    for (int w = 1; w < 32; w <<= 1) {
-      lo_all = max(lo_all, __shfl_xor_sync(kFull, lo_all, w));
-      hi_all = min(hi_all, __shfl_xor_sync(kFull, hi_all, w));
-    }
-    float m = -INFINITY;
-    float2 l2[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
     const uint32_t o_addr = tmem + lanes + C::kOCol + t * D;
-    bool ok = t < tiles;
-    for (int i = 0; ok && i < n; ++i) {
-      const int buf = C::kTiles == 2 ? t : (i & 1);
-      const uint32_t par = (C::kTiles == 2 ? i : i >> 1) & 1;
-      const uint32_t s_addr = tmem + lanes + buf * 128;
-      if (!(ok = mbar_wait_warp(s_full(buf), par, gave_up))) break;
-      fence_after();
-      uint32_t sv[128];
-#pragma unroll
-      for (int p = 0; p < 4; ++p) tmem_load32(s_addr + 32 * p, sv + 32 * p);
-      tmem_wait_load();
-      const uint32_t bad = s_bad[i % kBad];
-      const int k0 = i * kBlock;
-      const bool masked = k0 < lo_all || k0 + kBlock > hi_all || bad != 0;
-      if (masked) {
-#pragma unroll
-        for (int e = 0; e < 128; ++e)
-          if (k0 + e < lo || k0 + e >= hi || ((bad >> (e / 16)) & 1u)) sv[e] = 0xFF800000u;  // -inf
-      }
-      float tops[4];
-#pragma unroll
-      for (int y = 0; y < 4; ++y) {
-        tops[y] = fmaxf(__uint_as_float(sv[32 * y]), __uint_as_float(sv[32 * y + 1]));
-#pragma unroll
-        for (int e = 2; e < 32; e += 2)
-          tops[y] = fmax3(tops[y], __uint_as_float(sv[32 * y + e]), __uint_as_float(sv[32 * y + e + 1]));
-      }
-      const float top = fmaxf(fmax3(tops[0], tops[1], tops[2]), tops[3]) * c;
-      const bool raise = top > m + kRaise;
-      if (__any_sync(kFull, raise)) {
-        const float f = raise ? ex2(m - top) : 1.0f;
-        if (raise) m = top;
-#pragma unroll
-        for (int y = 0; y < 2; ++y) l2[y] = make_float2(l2[y].x * f, l2[y].y * f);
-        if (i > 0) {
-          // Tiles in turn: S of block i was issued after P V of block i - 1, so O
-          // is at rest.  Two S buffers: S of block i was issued after P V of block
-          // i - 2, so o_done has completed i - 1 or i times and the parity tells
-          // which; wait for the i-th.
-          if (C::kTiles == 1) {
-            if (!(ok = mbar_wait_warp(o_done, (i - 1) & 1, gave_up))) break;
-            fence_after();
-          }
+    int done = 0, seen = 0;  // blocks of this tile and of the CTA so far
+    uint32_t last = 0;       // parity of o_last
+    bool ok = true;
 #pragma unroll 1
-          for (int p = 0; p < D / 32; ++p) {
-            uint32_t ov[32];
+    for (int k = 0; ok && take(k); leave(k++)) {
+      const Item& it = s_item[k & 1];  // read again where it is used: the block loop needs the registers
+      const int n = it.blocks;
+      if (it.rows <= 128 * t) {
+        seen += n;
+        continue;
+      }
+      float c;
+      {
+        // The row, scaled by a power of two (and the score factor's sign), as f16.
+        const bool live = row < it.rows;
+        const int x = it.row0 + row, token = x / a.group;
+        const uint16_t* qp = a.q + int64_t(it.q0 + token) * a.ld_qt + int64_t(it.head * a.group + x - token * a.group) * a.ld_qh;
+        const bool vec = (reinterpret_cast<uintptr_t>(qp) & 15) == 0;
+        auto load8 = [&](int i) {
+          if (!live) return make_uint4(0u, 0u, 0u, 0u);
+          if (vec) return __ldg(reinterpret_cast<const uint4*>(qp) + i);
+          uint32_t w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) w[e] = uint32_t(qp[8 * i + 2 * e]) | (uint32_t(qp[8 * i + 2 * e + 1]) << 16);
+          return make_uint4(w[0], w[1], w[2], w[3]);
+        };
+        float amax = 0.0f;
+#pragma unroll 4
+        for (int i = 0; i < D / 8; ++i) {
+          float v[8];
+          unpack_bf16x8(load8(i), v);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(v[e]));
+        }
+        const float factor = a.scale_log2 * __ldg(a.k_scale);
+        const int e = int(__float_as_uint(amax) >> 23) - 127;
+        const int k = (amax == 0.0f || e > 127) ? 0 : min(14 - e, 100);
+        const float up = copysignf(__uint_as_float(uint32_t(k + 127) << 23), factor);
+        // At least the smallest normal number: 0 would make NaN of a masked key's -inf.
+        c = fmaxf(fabsf(factor) * __uint_as_float(uint32_t(127 - k) << 23), 1.17549435e-38f);
+        const uint32_t q_row = qs + t * C::kQBytes + (row & 127) * 128;
+#pragma unroll 4
+        for (int i = 0; i < D / 8; ++i) {
+          float v[8];
+          unpack_bf16x8(load8(i), v);
+          uint32_t h[4];
+#pragma unroll
+          for (int e2 = 0; e2 < 4; ++e2) h[e2] = pack_f16x2(v[2 * e2] * up, v[2 * e2 + 1] * up);
+          asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(q_row + (i >> 3) * 16384 + (((i & 7) ^ (row & 7)) << 4)),
+                       "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3])
+                       : "memory");
+        }
+        fence_smem_to_mma();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_full(t));
+      }
+      int lo = 0, hi = 0;  // keys in sight, relative to the first block
+      const bool live = row < it.rows;
+      if (live) {
+        const int64_t pos = int64_t(it.kv_len) - it.q_len + (it.row0 + row) / a.group;
+        hi = (a.causal ? int(min(int64_t(it.kv_len), max(int64_t(0), pos + 1))) : it.kv_len) - it.first;
+        lo = (a.window > 0 ? int(max(int64_t(0), pos + 1 - a.window)) : 0) - it.first;
+      }
+      // Blocks that every row of the warp sees whole need no mask.
+      int lo_all = live ? lo : -0x7fffffff, hi_all = live ? hi : 0x7fffffff;
+#pragma unroll
+      for (int w = 1; w < 32; w <<= 1) {
+        lo_all = max(lo_all, __shfl_xor_sync(kFull, lo_all, w));
+        hi_all = min(hi_all, __shfl_xor_sync(kFull, hi_all, w));
+      }
+      float m = -INFINITY;
+      float2 l2[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+      for (int i = 0; i < n; ++i, ++done, ++seen) {
+        const int buf = C::kTiles == 2 ? t : (done & 1);
+        const uint32_t par = (C::kTiles == 2 ? done : done >> 1) & 1;
+        const uint32_t s_addr = tmem + lanes + buf * 128;
+        if (!(ok = mbar_wait_warp(s_full(buf), par, gave_up))) break;
+        fence_after();
+        uint32_t sv[128];
+#pragma unroll
+        for (int p = 0; p < 4; ++p) tmem_load32(s_addr + 32 * p, sv + 32 * p);
+        tmem_wait_load();
+        const uint32_t bad = s_bad[seen % kBad];
+        const int k0 = i * kBlock;
+        const bool masked = k0 < lo_all || k0 + kBlock > hi_all || bad != 0;
+        if (masked) {
+#pragma unroll
+          for (int e = 0; e < 128; ++e)
+            if (k0 + e < lo || k0 + e >= hi || ((bad >> (e / 16)) & 1u)) sv[e] = 0xFF800000u;  // -inf
+        }
+        float tops[4];
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          tops[y] = fmaxf(__uint_as_float(sv[32 * y]), __uint_as_float(sv[32 * y + 1]));
+#pragma unroll
+          for (int e = 2; e < 32; e += 2)
+            tops[y] = fmax3(tops[y], __uint_as_float(sv[32 * y + e]), __uint_as_float(sv[32 * y + e + 1]));
+        }
+        const float top = fmaxf(fmax3(tops[0], tops[1], tops[2]), tops[3]) * c;
+        const bool raise = top > m + kRaise;
+        if (__any_sync(kFull, raise)) {
+          const float f = raise ? ex2(m - top) : 1.0f;
+          if (raise) m = top;
+#pragma unroll
+          for (int y = 0; y < 2; ++y) l2[y] = make_float2(l2[y].x * f, l2[y].y * f);
+          if (i > 0) {
+            // Tiles in turn: S of block i was issued after P V of block i - 1, so O
+            // is at rest.  Two S buffers: S of block i was issued after P V of block
+            // i - 2, so o_done has completed done - 1 or done times and the parity
+            // tells which; wait for the last.
+            if (C::kTiles == 1) {
+              if (!(ok = mbar_wait_warp(o_done, (done - 1) & 1, gave_up))) break;
+              fence_after();
+            }
+#pragma unroll 1
+            for (int p = 0; p < D / 32; ++p) {
+              uint32_t ov[32];
+              tmem_load32(o_addr + 32 * p, ov);
+              tmem_wait_load();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * f);
+              tmem_store32(o_addr + 32 * p, ov);
+            }
+            tmem_wait_store();
+          }
+        }
+        const float2 c2 = make_float2(c, c);
+        const float nm = m == -INFINITY ? 0.0f : -m;
+        const float2 nm2 = make_float2(nm, nm);
+        // Two halves of 64 keys, each handed over on its own, so that P V starts
+        // under the second half's exponentials.
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          uint32_t pv[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const float2 v = __ffma2_rn(
+                make_float2(__uint_as_float(sv[64 * p + 2 * e]), __uint_as_float(sv[64 * p + 2 * e + 1])), c2, nm2);
+            const float2 w = make_float2(ex2(v.x), ex2(v.y));
+            l2[e & 1] = __fadd2_rn(l2[e & 1], w);
+            pv[e] = pack_f16x2(w.x, w.y);
+          }
+          tmem_store32(s_addr + 32 * p, pv);
+          tmem_wait_store();
+          fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(p_full(buf, p));
+        }
+      }
+      // ---- output: this thread's row
+      if (ok && n > 0) {
+        ok = mbar_wait_warp(o_last(t), last, gave_up);
+        last ^= 1;
+        fence_after();
+      }
+      const float l = (l2[0].x + l2[0].y) + (l2[1].x + l2[1].y);
+      const int x = it.row0 + row, token = x / a.group, head = it.head * a.group + x - token * a.group;
+      const int64_t at = it.q0 + token;
+      float* part = nullptr;
+      if (a.splits > 1) part = partials_of(a) + (int64_t(it.index) * a.splits + it.split) * (C::kRows * (D + 2)) + row * D;
+      const float f = l > 0.0f || l != l ? __ldg(a.v_scale) / l : 0.0f;
+      if (ok) {
+#pragma unroll 1
+        for (int p = 0; p < D / 32; ++p) {
+          uint32_t ov[32];
+          if (n > 0) {
             tmem_load32(o_addr + 32 * p, ov);
             tmem_wait_load();
+          } else {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * f);
-            tmem_store32(o_addr + 32 * p, ov);
+            for (int e = 0; e < 32; ++e) ov[e] = 0u;
           }
-          tmem_wait_store();
+          if (!live) continue;
+          if (part != nullptr) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 4)
+              *reinterpret_cast<uint4*>(part + 32 * p + e) = make_uint4(ov[e], ov[e + 1], ov[e + 2], ov[e + 3]);
+            continue;
+          }
+          uint16_t* op = a.out + at * a.ld_ot + int64_t(head) * a.ld_oh + 32 * p;
+          uint32_t w[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            w[e] = pack_bf16x2(__uint_as_float(ov[2 * e]) * f, __uint_as_float(ov[2 * e + 1]) * f);
+          if ((reinterpret_cast<uintptr_t>(op) & 15) == 0) {
+#pragma unroll
+            for (int e = 0; e < 16; e += 4) *reinterpret_cast<uint4*>(op + 2 * e) = make_uint4(w[e], w[e + 1], w[e + 2], w[e + 3]);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) op[2 * e] = uint16_t(w[e]), op[2 * e + 1] = uint16_t(w[e] >> 16);
+          }
         }
-      }
-      const float2 c2 = make_float2(c, c);
-      const float nm = m == -INFINITY ? 0.0f : -m;
-      const float2 nm2 = make_float2(nm, nm);
-      // Two halves of 64 keys, each handed over on its own, so that P V starts
-      // under the second half's exponentials.
-#pragma unroll
-      for (int p = 0; p < 2; ++p) {
-        uint32_t pv[32];
-#pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          const float2 v = __ffma2_rn(
-              make_float2(__uint_as_float(sv[64 * p + 2 * e]), __uint_as_float(sv[64 * p + 2 * e + 1])), c2, nm2);
-          const float2 w = make_float2(ex2(v.x), ex2(v.y));
-          l2[e & 1] = __fadd2_rn(l2[e & 1], w);
-          pv[e] = pack_f16x2(w.x, w.y);
+        if (live) {
+          if (part != nullptr)
+            *reinterpret_cast<float2*>(part - row * D + C::kRows * D + 2 * row) = make_float2(m, l);
+          else if (a.lse != nullptr)
+            a.lse[at * a.ld_lse + head] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
         }
-        tmem_store32(s_addr + 32 * p, pv);
-        tmem_wait_store();
-        fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(p_full(buf, p));
-      }
-    }
-    // ---- output: this thread's row
-    if (ok && n > 0) {
-      ok = mbar_wait_warp(o_last(t), 0, gave_up);
-      fence_after();
-    }
-    const float l = (l2[0].x + l2[0].y) + (l2[1].x + l2[1].y);
-    const int64_t at = it.q0 + token;
-    float* part = nullptr;
-    if (a.splits > 1) part = partials_of(a) + (int64_t(it.index) * a.splits + it.split) * (C::kRows * (D + 2)) + row * D;
-    const float f = l > 0.0f || l != l ? __ldg(a.v_scale) / l : 0.0f;
-    if (ok) {
-#pragma unroll 1
-      for (int p = 0; p < D / 32; ++p) {
-        uint32_t ov[32];
-        if (n > 0) {
-          tmem_load32(o_addr + 32 * p, ov);
-          tmem_wait_load();
-        } else {
-#pragma unroll
-          for (int e = 0; e < 32; ++e) ov[e] = 0u;
-        }
-        if (!live) continue;
-        if (part != nullptr) {
-#pragma unroll
-          for (int e = 0; e < 32; e += 4)
-            *reinterpret_cast<uint4*>(part + 32 * p + e) = make_uint4(ov[e], ov[e + 1], ov[e + 2], ov[e + 3]);
-          continue;
-        }
-        uint16_t* op = a.out + at * a.ld_ot + int64_t(head) * a.ld_oh + 32 * p;
-        uint32_t w[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e)
-          w[e] = pack_bf16x2(__uint_as_float(ov[2 * e]) * f, __uint_as_float(ov[2 * e + 1]) * f);
-        if ((reinterpret_cast<uintptr_t>(op) & 15) == 0) {
-#pragma unroll
-          for (int e = 0; e < 16; e += 4) *reinterpret_cast<uint4*>(op + 2 * e) = make_uint4(w[e], w[e + 1], w[e + 2], w[e + 3]);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 16; ++e) op[2 * e] = uint16_t(w[e]), op[2 * e + 1] = uint16_t(w[e] >> 16);
-        }
-      }
-      if (live) {
-        if (part != nullptr)
-          *reinterpret_cast<float2*>(part - row * D + C::kRows * D + 2 * row) = make_float2(m, l);
-        else if (a.lse != nullptr)
-          a.lse[at * a.ld_lse + head] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
       }
     }
   } else if (warp < 12) {
@@ -579,108 +618,139 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
     if constexpr (C::kRegsProducer < 128) regs_dec<C::kRegsProducer>();
     constexpr int kMine = kAtoms / C::kProducerWarps;  // atoms of a block per warp
     const int pw = warp - 4 * C::kTiles;
-    const int32_t* table = a.table + int64_t(it.b) * a.ld_table;
-    const int64_t head_off = int64_t(it.head) * (int64_t(KvAtom<D>::kBytes) << (a.cache.log_page - 4));
-    auto token_of = [&](int block, int i) { return it.first + block * kBlock + 16 * (pw + C::kProducerWarps * i); };
-    // Pages of this warp's atoms of a block; -1: none (out of the cache), -2: behind the last key.
-    struct Pages {
-      int32_t of[kMine];
-    };
-    auto pages_of = [&](int block) {
-      Pages p;
-#pragma unroll
-      for (int i = 0; i < kMine; ++i) {
-        const int t = token_of(block, i);
-        p.of[i] = -2;
-        if (block < n && t < it.kv_len) {
-          const int32_t page = __ldg(table + (t >> a.cache.log_page));
-          p.of[i] = page < 0 || page >= a.cache.pages ? -1 : page;
-        }
-      }
-      return p;
-    };
-    struct Raw {
-      RawAtom<D> atom[kMine];
-    };
-    auto fetch = [&](Raw& raw, int block, const Pages& p, bool value) {
-#pragma unroll
-      for (int i = 0; i < kMine; ++i) {
-        const int t = token_of(block, i);
-        const uint8_t* atom = p.of[i] < 0 ? nullptr
-                                          : a.cache.base + p.of[i] * a.cache.page_stride + head_off +
-                                                ((t & ((1 << a.cache.log_page) - 1)) >> 4) * KvAtom<D>::kBytes;
-        load_atom<D>(raw.atom[i], atom, value, lane);
-      }
-    };
-    int q = 0;  // item of the stream; its slot
+    int q = 0, seen = 0;  // blocks of K and V filled, blocks of the items before
     bool ok = true;
-    auto convert = [&](const Raw& raw, int block, bool value) {
-      const int slot = q % C::kSlots, round = q / C::kSlots;
-      ++q;
-      if (C::kTiles == 2) {
-        // Releases: 0 of K(0), then 1 + i of V(i) and K(i + 1) together, counted
-        // over eight barriers.
-        const int release = (value ? block + 1 : block) - C::kSlots / 2;
-        if (round > 0 && !(ok = mbar_wait_warp(empty(release % 8), (release / 8) & 1, gave_up))) return;
-      } else {
-        if (round > 0 && !(ok = mbar_wait_warp(empty(slot), (round - 1) & 1, gave_up))) return;
-      }
+#pragma unroll 1
+    for (int k = 0; ok && take(k); ++k) {
+      const Item it = s_item[k & 1];
+      leave(k);
+      const int n = it.blocks;
+      const int32_t* table = a.table + int64_t(it.b) * a.ld_table;
+      const int64_t head_off = int64_t(it.head) * (int64_t(KvAtom<D>::kBytes) << (a.cache.log_page - 4));
+      auto token_of = [&](int block, int i) { return it.first + block * kBlock + 16 * (pw + C::kProducerWarps * i); };
+      // Pages of this warp's atoms of a block; -1: none (out of the cache), -2: behind the last key.
+      struct Pages {
+        int32_t of[kMine];
+      };
+      auto pages_of = [&](int block) {
+        Pages p;
 #pragma unroll
-      for (int i = 0; i < kMine; ++i)
-        convert_atom<D>(raw.atom[i], ring + slot * C::kSlotBytes, 16 * (pw + C::kProducerWarps * i), value,
-                        it.kv_len - token_of(block, i), lane);
-      fence_smem_to_mma();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(full(slot));
-    };
-    // Atoms without a page: their keys count as out of sight.  Written before
-    // the block's K slot is filled.
-    auto note_missing = [&](int block, const Pages& p) {
-#pragma unroll
-      for (int i = 0; i < kMine; ++i) {
-        const uint32_t bit = 1u << (pw + C::kProducerWarps * i);
-        if (lane == 0) {
-          if (p.of[i] == -1) {
-            atomicOr(&s_bad[block % kBad], bit);
-            atomicOr(a.err, kErrSlot);
-          } else {
-            atomicAnd(&s_bad[block % kBad], ~bit);
+        for (int i = 0; i < kMine; ++i) {
+          const int t = token_of(block, i);
+          p.of[i] = -2;
+          if (block < n && t < it.kv_len) {
+            const int32_t page = __ldg(table + (t >> a.cache.log_page));
+            p.of[i] = page < 0 || page >= a.cache.pages ? -1 : page;
           }
         }
+        return p;
+      };
+      struct Raw {
+        RawAtom<D> atom[kMine];
+      };
+      auto fetch = [&](Raw& raw, int block, const Pages& p, bool value) {
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) {
+          const int t = token_of(block, i);
+          const uint8_t* atom = p.of[i] < 0 ? nullptr
+                                            : a.cache.base + p.of[i] * a.cache.page_stride + head_off +
+                                                  ((t & ((1 << a.cache.log_page) - 1)) >> 4) * KvAtom<D>::kBytes;
+          load_atom<D>(raw.atom[i], atom, value, lane);
+        }
+      };
+      auto convert = [&](const Raw& raw, int block, bool value) {
+        const int slot = q % C::kSlots, round = q / C::kSlots;
+        ++q;
+        if (round > 0 && !(ok = mbar_wait_warp(empty(slot), (round - 1) & 1, gave_up))) return;
+#pragma unroll
+        for (int i = 0; i < kMine; ++i)
+          convert_atom<D>(raw.atom[i], ring + slot * C::kSlotBytes, 16 * (pw + C::kProducerWarps * i), value,
+                          it.kv_len - token_of(block, i), lane);
+        fence_smem_to_mma();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(full(slot));
+      };
+      // Atoms without a page: their keys count as out of sight.  Written before
+      // the block's K slot is filled.
+      auto note_missing = [&](int block, const Pages& p) {
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) {
+          const uint32_t bit = 1u << (pw + C::kProducerWarps * i);
+          if (lane == 0) {
+            if (p.of[i] == -1) {
+              atomicOr(&s_bad[(seen + block) % kBad], bit);
+              atomicOr(a.err, kErrSlot);
+            } else {
+              atomicAnd(&s_bad[(seen + block) % kBad], ~bit);
+            }
+          }
+        }
+      };
+      // The stream: tiles in turn K0 V0 K1 V1 ..., two S buffers K0 K1 V0 K2 V1 ...
+      // The bytes of the next block's keys (values) are on their way while this
+      // block's are converted, and the pages of the block after that.
+      Raw raw_k, raw_v;
+      Pages now = pages_of(0), next = pages_of(1), later = pages_of(2);
+      fetch(raw_k, 0, now, false);
+      fetch(raw_v, 0, now, true);
+      // Near the end, and not before, the CTA claims its next item: whoever is free first gets it.
+      const int due = max(0, n - 5);
+      if (n == 0 && pw == 0 && lane == 0) mbar_arrive(item_due);
+      if (C::kTiles == 1 && n > 0) {
+        note_missing(0, now);
+        convert(raw_k, 0, false);
+        fetch(raw_k, 1, next, false);
       }
-    };
-    // The stream: tiles in turn K0 V0 K1 V1 ..., two S buffers K0 K1 V0 K2 V1 ...
-    // The bytes of the next block's keys (values) are on their way while this
-    // block's are converted, and the pages of the block after that.
-    Raw raw_k, raw_v;
-    Pages now = pages_of(0), next = pages_of(1), later = pages_of(2);
-    fetch(raw_k, 0, now, false);
-    fetch(raw_v, 0, now, true);
-    if (C::kTiles == 1 && n > 0) {
-      note_missing(0, now);
-      convert(raw_k, 0, false);
-      fetch(raw_k, 1, next, false);
-    }
-    for (int i = 0; i < n && ok; ++i) {
-      const int kb = C::kTiles == 2 ? i : i + 1;
-      if (kb < n) {
-        const Pages& kp = C::kTiles == 2 ? now : next;
-        note_missing(kb, kp);
-        convert(raw_k, kb, false);
+      for (int i = 0; i < n && ok; ++i) {
+        const int kb = C::kTiles == 2 ? i : i + 1;
+        if (i == due && pw == 0 && lane == 0) mbar_arrive(item_due);
+        if (kb < n) {
+          const Pages& kp = C::kTiles == 2 ? now : next;
+          note_missing(kb, kp);
+          convert(raw_k, kb, false);
+          if (!ok) break;
+          fetch(raw_k, kb + 1, C::kTiles == 2 ? next : later, false);
+        }
+        convert(raw_v, i, true);
         if (!ok) break;
-        fetch(raw_k, kb + 1, C::kTiles == 2 ? next : later, false);
+        fetch(raw_v, i + 1, next, true);
+        now = next;
+        next = later;
+        later = pages_of(i + 3);
       }
-      convert(raw_v, i, true);
-      if (!ok) break;
-      fetch(raw_v, i + 1, next, true);
-      now = next;
-      next = later;
-      later = pages_of(i + 3);
+      seen += n;
     }
   } else {
-    // ----------------------------------------------------------- products ----
     regs_dec<C::kRegsMma>();
-    if (warp == 12 && n > 0) {
+    if (warp == 13) {
+      // ------------------------------------------------------------- items ----
+      // The next item is found while this one is worked on.  The first is the
+      // CTA's own number, further ones are claimed.
+      const int total = a.tiles * a.cache.heads * a.splits;
+      int next = int(blockIdx.x);
+      bool ok = true;
+      for (int k = 0; ok; ++k) {
+        Item it{};
+        if (k > 0 && !(ok = mbar_wait_warp<true>(item_due, (k - 1) & 1, gave_up))) break;
+        while (true) {
+          if (next < 0) {
+            if (lane == 0) next = int(gridDim.x + atomicAdd(claims_of(a), 1u));
+            next = __shfl_sync(kFull, next, 0);
+          }
+          if (next >= total) break;
+          it = find_item<C::kRows>(a, next, lane);
+          next = -1;
+          if (it.rows > 0) break;
+        }
+        if (k > 1 && !(ok = mbar_wait_warp<true>(item_empty(k & 1), ((k >> 1) - 1) & 1, gave_up))) break;
+        if (lane == 0) {
+          s_item[k & 1] = it;
+          mbar_arrive(item_full(k & 1));
+        }
+        if (it.rows == 0) break;
+      }
+    } else if (warp == 12) {
+      // ---------------------------------------------------------- products ----
       // The whole warp walks the loop, so that descriptors and counters stay in
       // uniform registers; one elected lane issues.  Rolled loops: this code runs
       // for a moment between long waits, and unrolled it was slowed to 100 cycles
@@ -688,8 +758,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
       const bool leader = elect_one();
       const uint32_t tm = __shfl_sync(kFull, tmem, 0);
       constexpr uint32_t kIdQK = instruction(kBlock, false), kIdPV = instruction(D, true);
-      bool ok = mbar_wait_warp(q_full, 0, gave_up);
-      fence_after();
+      bool ok = true;
       auto wait_slot = [&](int q) {
         ok = ok && mbar_wait_warp(full(q % C::kSlots), (q / C::kSlots) & 1, gave_up);
         fence_after();
@@ -728,62 +797,83 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
           vd += 8192 >> 4;
         }
       };
-      if constexpr (C::kTiles == 2) {
-        wait_slot(0);
-        for (int t = 0; t < tiles && ok; ++t) {
-          qk(t, 128 * t, 0);
-          arrive(s_full(t));
-        }
-        if (ok) arrive(empty(0));
+      int q = 0, done = 0;                // blocks of K and V used; S buffers filled (two buffers)
+      uint32_t p_par = 0, q_par = 0;      // bit t: parity of p_full (tiles in turn) and q_full of tile t
 #pragma unroll 1
-        for (int i = 0; i < n && ok; ++i) {
-          // The producers fill V(i) before K(i + 1): one wait covers both.
-          const int qv = 2 * i + 1, qn = 2 * i + 2;
-          wait_slot(i + 1 < n ? qn : qv);
-#pragma unroll 1
+      for (int item = 0; ok && take(item); ++item) {
+        const int n = s_item[item & 1].blocks, tiles = s_item[item & 1].rows > 128 ? 2 : 1;
+        leave(item);
+        const uint32_t both = uint32_t(tiles) | 1u;  // bit t: tile t has rows
+        const uint32_t q_now = q_par;
+        q_par ^= both;
+        if (n == 0) continue;
+        auto wait_q = [&](int t) {
+          ok = ok && mbar_wait_warp(q_full(t), (q_now >> t) & 1, gave_up);
+          fence_after();
+        };
+        wait_slot(q);
+        if constexpr (C::kTiles == 2) {
           for (int t = 0; t < tiles && ok; ++t) {
-            pv(t, t, i & 1, qv, i == 0);
-            if (ok && i + 1 < n) {
-              qk(t, 128 * t, qn);
-              arrive(s_full(t));
-            }
-          }
-          if (ok) arrive(empty((i + 1) % 8));  // V(i) and K(i + 1)
-        }
-        for (int t = 0; t < tiles && ok; ++t) arrive(o_last(t));
-      } else {
-        // K0 K1 V0 K2 V1 ... K(n-1) V(n-2) V(n-1)
-        wait_slot(0);
-        if (ok) {
-          qk(0, 0, 0);
-          arrive(s_full(0));
-          arrive(empty(0));
-        }
-        int q = 1;
-#pragma unroll 1
-        for (int i = 0; i < n && ok; ++i) {
-          if (i + 1 < n) {
-            wait_slot(q);
+            wait_q(t);
             if (!ok) break;
-            qk(0, 128 * ((i + 1) & 1), q);
-            arrive(s_full((i + 1) & 1));
-            arrive(empty(q % C::kSlots));
-            ++q;
+            qk(t, 128 * t, q);
+            arrive(s_full(t));
           }
-          wait_slot(q);
+          if (ok) arrive(empty(q % C::kSlots));
+#pragma unroll 1
+          for (int i = 0; i < n && ok; ++i) {
+            // The producers fill V(i) before K(i + 1): one wait covers both.
+            const int qv = q + 2 * i + 1, qn = qv + 1;
+            wait_slot(i + 1 < n ? qn : qv);
+#pragma unroll 1
+            for (int t = 0; t < tiles && ok; ++t) {
+              pv(t, t, ((p_par >> t) ^ uint32_t(i)) & 1, qv, i == 0);
+              if (!ok) break;
+              if (i + 1 < n) qk(t, 128 * t, qn);
+              arrive(i + 1 < n ? s_full(t) : o_last(t));
+            }
+            if (!ok) break;
+            arrive(empty(qv % C::kSlots));
+            if (i + 1 < n) arrive(empty(qn % C::kSlots));
+          }
+          if (n & 1) p_par ^= both;
+        } else {
+          // K0 K1 V0 K2 V1 ... K(n-1) V(n-2) V(n-1)
+          wait_q(0);
           if (!ok) break;
-          pv(0, i & 1, (i >> 1) & 1, q, i == 0);
-          if (!ok) break;
-          arrive(empty(q % C::kSlots));
-          arrive(o_done);
-          ++q;
+          int at = q;
+          qk(0, 128 * (done & 1), at);
+          arrive(s_full(done & 1));
+          arrive(empty(at % C::kSlots));
+          ++at;
+#pragma unroll 1
+          for (int i = 0; i < n && ok; ++i) {
+            const int buf = (done + i) & 1;
+            if (i + 1 < n) {
+              wait_slot(at);
+              if (!ok) break;
+              qk(0, 128 * (buf ^ 1), at);
+              arrive(s_full(buf ^ 1));
+              arrive(empty(at % C::kSlots));
+              ++at;
+            }
+            wait_slot(at);
+            if (!ok) break;
+            pv(0, buf, ((done + i) >> 1) & 1, at, i == 0);
+            if (!ok) break;
+            arrive(empty(at % C::kSlots));
+            arrive(o_done);
+            ++at;
+          }
+          done += n;
+          if (ok) arrive(o_last(0));
         }
-        if (ok) arrive(o_last(0));
+        q += 2 * n;
       }
-      if (!ok) {
+      if (__any_sync(kFull, !ok || *gave_up)) {
         // Products in flight end before their tensor memory is freed.
-        arrive(drained(warp - 12));
-        for (int i = 0; i < (1 << 20) && !mbar_try(drained(warp - 12), 0); ++i) {
+        arrive(drained);
+        for (int i = 0; i < (1 << 20) && !mbar_try(drained, 0); ++i) {
         }
       }
     }
@@ -791,7 +881,11 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
   }
   fence_before();
   __syncthreads();
-  if (tid == 0 && s_gave_up) atomicOr(a.err, kErrWait);
+  if (tid == 0) {
+    if (s_gave_up) atomicOr(a.err, kErrWait);
+    // The last CTA leaves the counters at zero (its own wraps around).
+    if (atomicInc(done_of(a), gridDim.x - 1) == gridDim.x - 1) *claims_of(a) = 0;
+  }
   if (warp == 12) {
     fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
@@ -802,12 +896,11 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
 template <int D>
 __global__ void __launch_bounds__(256) join_kernel(const AttnArgs a) {
   constexpr int R = Cfg<D>::kRows, kSlot = R * (D + 2);
-  __shared__ int s_found;
   griddep_wait();
   griddep_launch_dependents();
   const int part = int(blockIdx.x) % (R / 8);
-  const Item it = find_item<R>(a, int(blockIdx.x) / (R / 8) * a.splits, a.tiles, 256, &s_found);
   const int row = part * 8 + int(threadIdx.x >> 5), lane = int(threadIdx.x) & 31;
+  const Item it = find_item<R>(a, int(blockIdx.x) / (R / 8) * a.splits, lane);
   if (row >= it.rows) return;
   const int x = it.row0 + row, token = x / a.group, head = it.head * a.group + x - token * a.group;
   const float* base = partials_of(a) + int64_t(it.index) * a.splits * kSlot;

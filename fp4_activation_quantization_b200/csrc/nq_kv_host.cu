@@ -262,7 +262,7 @@ nq_status nq_attention_nvfp4_kv(const void* q, int64_t ld_q_token, int64_t ld_q_
     a.tiles = int32_t(tiles);
     a.splits = int32_t(splits);
     void* args[] = {&a};
-    nq_status s = nq::host::launch(fn, t.kernel, unsigned(ctas), nq::kAttnTilesThreads, t.smem, args,
+    nq_status s = nq::host::launch(fn, t.kernel, unsigned(ctas < sms ? ctas : sms), nq::kAttnTilesThreads, t.smem, args,
                                    (flags & NQ_FLAG_PDL) != 0, static_cast<cudaStream_t>(stream));
     if (s == NQ_OK && splits > 1)
       s = nq::host::launch(fn, t.join, unsigned(join_grid), 256, 0, args, (flags & NQ_FLAG_PDL) != 0,
