@@ -22,11 +22,17 @@
 //
 // A warp finds the next item while this one is worked on, the producers go on to
 // its keys while the last blocks are multiplied, and the barriers count on, so that
-// between items only the output and the queries stand still.  (A CTA per item paid
-// about 10 us at each end: 16 chunks of 512 behind 1536 tokens, heads of 128 332 us,
-// now 317; of 256 385, now 356; of 64 506, now 461.)  Items are claimed when five
-// blocks of the item before are left: earlier, the last items went to CTAs that
-// were not the first to be free (252 us instead of 172 for 256 items).
+// between items only the output and the queries stand still.  (With a CTA per item,
+// 16 chunks of 512 behind 1536 tokens, 8 kv heads: of 128 332 us, now 315; of 256
+// 385, now 358; of 64 506, now 465.)  A prompt of 8192, 32/8 heads of 128: 552 us, 996
+// TFLOP/s, 0.62 of the measured product rate; a block of 128 keys takes the CTA
+// about 4400 cycles, of which products, exponentials and the conversion's way
+// through shared memory are about 2000 each and overlap in part.  One tile alone
+// (an item of at most 128 rows) still takes 3900 a block; with its keys shared out
+// between two tiles of the same rows, 24 x 64 rows over 4096 keys took 133 us
+// instead of 141, but items of two tiles lost 3 to 7 %.  Items are claimed when
+// five blocks of the item before are left: earlier, the last items went to CTAs
+// that were not the first to be free (256 items of 33 blocks: 252 us, now 168).
 //
 // Every wait on an mbarrier is bounded; a CTA whose wait runs out records it in
 // the device error word, frees its tensor memory and leaves.
@@ -55,8 +61,8 @@ struct Cfg {
   static constexpr int kSmem = 131072 + kTiles * kQBytes + 1024;  // 1024: alignment
   // Registers of a thread after the split; the launch holds 512 x 128, so a
   // role above 128 asks for more and one below 128 gives some up.
-  static constexpr int kRegsSoftmax = D == 256 ? 224 : 184;
-  static constexpr int kRegsProducer = D == 256 ? 128 : 112;
+  static constexpr int kRegsSoftmax = D == 256 ? 224 : 192;
+  static constexpr int kRegsProducer = D == 256 ? 128 : 96;
   static constexpr int kRegsMma = 32;
   static_assert(kRegsSoftmax > 128 && kRegsProducer <= 128 && kRegsMma < 128, "direction of the split");
   static_assert(kTiles * kRegsSoftmax + (3 - kTiles) * kRegsProducer + kRegsMma <= 4 * 128, "register split");
@@ -171,6 +177,7 @@ struct Item {
   int q0, q_len, kv_len;
   int first, blocks;  // first key (a multiple of 16), blocks of this split
   int index, split;   // number of the item among tiles and heads, of the split
+  int before;         // blocks of the CTA's items before
 };
 
 __device__ __forceinline__ float* partials_of(const AttnArgs& a) { return reinterpret_cast<float*>(a.workspace + kAttnHeader); }
@@ -413,17 +420,13 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
     const int t = warp >> 2, row = tid;  // row of the item; tile t's thread holds lane row % 128
     const uint32_t lanes = uint32_t(warp & 3) << 21;  // tensor memory: lane in the upper half
     const uint32_t o_addr = tmem + lanes + C::kOCol + t * D;
-    int done = 0, seen = 0;  // blocks of this tile and of the CTA so far
-    uint32_t last = 0;       // parity of o_last
+    uint32_t done = 0;  // blocks of this tile so far; bit 31: parity of o_last
     bool ok = true;
 #pragma unroll 1
     for (int k = 0; ok && take(k); leave(k++)) {
       const Item& it = s_item[k & 1];  // read again where it is used: the block loop needs the registers
       const int n = it.blocks;
-      if (it.rows <= 128 * t) {
-        seen += n;
-        continue;
-      }
+      if (it.rows <= 128 * t) continue;
       float c;
       {
         // The row, scaled by a power of two (and the score factor's sign), as f16.
@@ -485,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
       }
       float m = -INFINITY;
       float2 l2[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-      for (int i = 0; i < n; ++i, ++done, ++seen) {
+      for (int i = 0; i < n; ++i, ++done) {
         const int buf = C::kTiles == 2 ? t : (done & 1);
         const uint32_t par = (C::kTiles == 2 ? done : done >> 1) & 1;
         const uint32_t s_addr = tmem + lanes + buf * 128;
@@ -495,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
 #pragma unroll
         for (int p = 0; p < 4; ++p) tmem_load32(s_addr + 32 * p, sv + 32 * p);
         tmem_wait_load();
-        const uint32_t bad = s_bad[seen % kBad];
+        const uint32_t bad = s_bad[(it.before + i) % kBad];
         const int k0 = i * kBlock;
         const bool masked = k0 < lo_all || k0 + kBlock > hi_all || bad != 0;
         if (masked) {
@@ -564,8 +567,8 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
       }
       // ---- output: this thread's row
       if (ok && n > 0) {
-        ok = mbar_wait_warp(o_last(t), last, gave_up);
-        last ^= 1;
+        ok = mbar_wait_warp(o_last(t), done >> 31, gave_up);
+        done ^= 1u << 31;
         fence_after();
       }
       const float l = (l2[0].x + l2[0].y) + (l2[1].x + l2[1].y);
@@ -618,7 +621,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
     if constexpr (C::kRegsProducer < 128) regs_dec<C::kRegsProducer>();
     constexpr int kMine = kAtoms / C::kProducerWarps;  // atoms of a block per warp
     const int pw = warp - 4 * C::kTiles;
-    int q = 0, seen = 0;  // blocks of K and V filled, blocks of the items before
+    int q = 0;  // blocks of K and V filled
     bool ok = true;
 #pragma unroll 1
     for (int k = 0; ok && take(k); ++k) {
@@ -658,6 +661,20 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
           load_atom<D>(raw.atom[i], atom, value, lane);
         }
       };
+      // A block's bytes on their way to L2, as from HBM they take longer than a block: 32 chunks of 64 tokens over
+      // 4096 keys 172 -> 168 us.  (With heads of 256 a prompt of 8192 lost, 576 -> 594: off there.)
+      auto warm = [&](int block, const Pages& p) {
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) {
+          const int t = token_of(block, i);
+          const uint8_t* atom = a.cache.base + p.of[i] * a.cache.page_stride + head_off +
+                                ((t & ((1 << a.cache.log_page) - 1)) >> 4) * KvAtom<D>::kBytes;
+#pragma unroll
+          for (int at = 0; at < KvAtom<D>::kBytes; at += 4096)
+            if (p.of[i] >= 0 && at + 128 * lane < KvAtom<D>::kBytes)
+              asm volatile("prefetch.global.L2 [%0];" ::"l"(atom + at + 128 * lane));
+        }
+      };
       auto convert = [&](const Raw& raw, int block, bool value) {
         const int slot = q % C::kSlots, round = q / C::kSlots;
         ++q;
@@ -678,10 +695,10 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
           const uint32_t bit = 1u << (pw + C::kProducerWarps * i);
           if (lane == 0) {
             if (p.of[i] == -1) {
-              atomicOr(&s_bad[(seen + block) % kBad], bit);
+              atomicOr(&s_bad[(it.before + block) % kBad], bit);
               atomicOr(a.err, kErrSlot);
             } else {
-              atomicAnd(&s_bad[(seen + block) % kBad], ~bit);
+              atomicAnd(&s_bad[(it.before + block) % kBad], ~bit);
             }
           }
         }
@@ -693,6 +710,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
       Pages now = pages_of(0), next = pages_of(1), later = pages_of(2);
       fetch(raw_k, 0, now, false);
       fetch(raw_v, 0, now, true);
+      if (C::kTiles == 2) warm(1, next);
       // Near the end, and not before, the CTA claims its next item: whoever is free first gets it.
       const int due = max(0, n - 5);
       if (n == 0 && pw == 0 && lane == 0) mbar_arrive(item_due);
@@ -703,6 +721,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
       }
       for (int i = 0; i < n && ok; ++i) {
         const int kb = C::kTiles == 2 ? i : i + 1;
+        if (C::kTiles == 2) warm(i + 2, later);
         if (i == due && pw == 0 && lane == 0) mbar_arrive(item_due);
         if (kb < n) {
           const Pages& kp = C::kTiles == 2 ? now : next;
@@ -718,7 +737,6 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
         next = later;
         later = pages_of(i + 3);
       }
-      seen += n;
     }
   } else {
     regs_dec<C::kRegsMma>();
@@ -727,7 +745,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
       // The next item is found while this one is worked on.  The first is the
       // CTA's own number, further ones are claimed.
       const int total = a.tiles * a.cache.heads * a.splits;
-      int next = int(blockIdx.x);
+      int next = int(blockIdx.x), before = 0;
       bool ok = true;
       for (int k = 0; ok; ++k) {
         Item it{};
@@ -743,6 +761,8 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
           if (it.rows > 0) break;
         }
         if (k > 1 && !(ok = mbar_wait_warp<true>(item_empty(k & 1), ((k >> 1) - 1) & 1, gave_up))) break;
+        it.before = before;
+        before += it.blocks;
         if (lane == 0) {
           s_item[k & 1] = it;
           mbar_arrive(item_full(k & 1));

@@ -258,7 +258,7 @@ nq_status nq_attention_nvfp4_kv(const void* q, int64_t ld_q_token, int64_t ld_q_
     splits = splits < blocks ? splits : blocks;
     splits = splits < 1 ? 1 : splits;
     const int64_t ctas = items * splits, join_grid = items * (t.rows / 8);
-    if (ctas > kInt32Max || join_grid > kInt32Max) return error(NQ_ERR_UNSUPPORTED, "%s: T or B too large", fn);
+    if (ctas > kInt32Max - 2 * sms || join_grid > kInt32Max) return error(NQ_ERR_UNSUPPORTED, "%s: T or B too large", fn);
     a.tiles = int32_t(tiles);
     a.splits = int32_t(splits);
     void* args[] = {&a};
