@@ -433,49 +433,65 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
         const bool live = row < it.rows;
         const int x = it.row0 + row, token = x / a.group;
         const uint16_t* qp = a.q + int64_t(it.q0 + token) * a.ld_qt + int64_t(it.head * a.group + x - token * a.group) * a.ld_qh;
-        const bool vec = (reinterpret_cast<uintptr_t>(qp) & 15) == 0;
-        // All of it at once: in turns of four loads a row of 256 took 8 us.
-        uint4 raw[D / 8];
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i) raw[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (live && vec) {
-#pragma unroll
-          for (int i = 0; i < D / 8; ++i) raw[i] = __ldg(reinterpret_cast<const uint4*>(qp) + i);
-        } else if (live) {
-#pragma unroll
-          for (int i = 0; i < D / 8; ++i) {
-            uint32_t w[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) w[e] = uint32_t(qp[8 * i + 2 * e]) | (uint32_t(qp[8 * i + 2 * e + 1]) << 16);
-            raw[i] = make_uint4(w[0], w[1], w[2], w[3]);
-          }
-        }
-        float amax = 0.0f;
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-          float v[8];
-          unpack_bf16x8(raw[i], v);
+        // A warp's 32 rows, D / 8 lanes to a row, 16 loads on their way at once (a
+        // thread's own row in turns of four: 8 us an item).
+        constexpr int kLanes = D / 8, kPer = 32 / kLanes, kBatch = kLanes < 16 ? kLanes : 16;
+        const uint64_t own = live ? reinterpret_cast<uint64_t>(qp) : 0;
+        const float factor = a.scale_log2 * __ldg(a.k_scale);
+        auto power = [](float amax) {  // of two, to which the row's largest is scaled
+          const int e = int(__float_as_uint(amax) >> 23) - 127;
+          return amax == 0.0f || e > 127 ? 0 : min(14 - e, 100);
+        };
+        const uint32_t q_tile = qs + t * C::kQBytes;
+        float mine = 0.0f;  // this thread's row's largest
+        auto put = [&](const uint4& raw, int i) {  // rows i kPer ... of the warp
+          float v[8], amax = 0.0f;
+          unpack_bf16x8(raw, v);
 #pragma unroll
           for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(v[e]));
-        }
-        const float factor = a.scale_log2 * __ldg(a.k_scale);
-        const int e = int(__float_as_uint(amax) >> 23) - 127;
-        const int k = (amax == 0.0f || e > 127) ? 0 : min(14 - e, 100);
-        const float up = copysignf(__uint_as_float(uint32_t(k + 127) << 23), factor);
-        // At least the smallest normal number: 0 would make NaN of a masked key's -inf.
-        c = fmaxf(fabsf(factor) * __uint_as_float(uint32_t(127 - k) << 23), 1.17549435e-38f);
-        const uint32_t q_row = qs + t * C::kQBytes + (row & 127) * 128;
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-          float v[8];
-          unpack_bf16x8(raw[i], v);
+          for (int o = 1; o < kLanes; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, o));
+          const float row_max = __shfl_sync(kFull, amax, (lane % kPer) * kLanes);
+          if (lane / kPer == i) mine = row_max;
+          const float up = copysignf(__uint_as_float(uint32_t(power(amax) + 127) << 23), factor);
           uint32_t h[4];
 #pragma unroll
           for (int e2 = 0; e2 < 4; ++e2) h[e2] = pack_f16x2(v[2 * e2] * up, v[2 * e2 + 1] * up);
-          asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(q_row + (i >> 3) * 16384 + (((i & 7) ^ (row & 7)) << 4)),
+          const int at = (warp & 3) * 32 + i * kPer + lane / kLanes, piece = lane % kLanes;
+          asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(q_tile + (piece >> 3) * 16384 + at * 128 +
+                                                                       (((piece & 7) ^ (at & 7)) << 4)),
                        "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3])
                        : "memory");
+        };
+        auto from = [&](int i) {
+          const uint64_t row_p = __shfl_sync(kFull, own, i * kPer + lane / kLanes);
+          return row_p ? reinterpret_cast<const uint16_t*>(row_p) + 8 * (lane % kLanes) : nullptr;
+        };
+        if (__all_sync(kFull, (own & 15) == 0)) {
+#pragma unroll 1
+          for (int b = 0; b < kLanes; b += kBatch) {
+            uint4 raw[kBatch];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+              const uint16_t* p = from(b + i);
+              raw[i] = p ? __ldg(reinterpret_cast<const uint4*>(p)) : make_uint4(0u, 0u, 0u, 0u);
+            }
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) put(raw[i], b + i);
+          }
+        } else {
+#pragma unroll 1
+          for (int i = 0; i < kLanes; ++i) {
+            const uint16_t* p = from(i);
+            uint32_t w[4] = {0u, 0u, 0u, 0u};
+            if (p)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) w[e] = uint32_t(p[2 * e]) | (uint32_t(p[2 * e + 1]) << 16);
+            put(make_uint4(w[0], w[1], w[2], w[3]), i);
+          }
         }
+        // At least the smallest normal number: 0 would make NaN of a masked key's -inf.
+        c = fmaxf(fabsf(factor) * __uint_as_float(uint32_t(127 - power(mine)) << 23), 1.17549435e-38f);
         fence_smem_to_mma();
         __syncwarp();
         if (lane == 0) mbar_arrive(q_full(t));
