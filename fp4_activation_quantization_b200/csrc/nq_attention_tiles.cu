@@ -601,6 +601,9 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
       float* part = nullptr;
       if (a.splits > 1) part = partials_of(a) + (int64_t(it.index) * a.splits + it.split) * (C::kRows * (D + 2)) + row * D;
       const float f = l > 0.0f || l != l ? __ldg(a.v_scale) / l : 0.0f;
+      uint16_t* orow = a.out + at * a.ld_ot + int64_t(head) * a.ld_oh;
+      const uint64_t own = live ? reinterpret_cast<uint64_t>(orow) : 0;
+      const bool wide = part == nullptr && __all_sync(kFull, (own & 15) == 0);
       if (ok) {
 #pragma unroll 1
         for (int p = 0; p < D / 32; ++p) {
@@ -612,6 +615,21 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
 #pragma unroll
             for (int e = 0; e < 32; ++e) ov[e] = 0u;
           }
+          if (wide) {  // over the tile's queries, whose products are done
+            uint32_t w[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              w[e] = pack_bf16x2(__uint_as_float(ov[2 * e]) * f, __uint_as_float(ov[2 * e + 1]) * f);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int piece = 4 * p + e;
+              asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(qs + t * C::kQBytes + (piece >> 3) * 16384 + (row & 127) * 128 +
+                                                                           (((piece & 7) ^ (row & 7)) << 4)),
+                           "r"(w[4 * e]), "r"(w[4 * e + 1]), "r"(w[4 * e + 2]), "r"(w[4 * e + 3])
+                           : "memory");
+            }
+            continue;
+          }
           if (!live) continue;
           if (part != nullptr) {
 #pragma unroll
@@ -619,17 +637,23 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
               *reinterpret_cast<uint4*>(part + 32 * p + e) = make_uint4(ov[e], ov[e + 1], ov[e + 2], ov[e + 3]);
             continue;
           }
-          uint16_t* op = a.out + at * a.ld_ot + int64_t(head) * a.ld_oh + 32 * p;
-          uint32_t w[16];
+          uint16_t* op = orow + 32 * p;
 #pragma unroll
-          for (int e = 0; e < 16; ++e)
-            w[e] = pack_bf16x2(__uint_as_float(ov[2 * e]) * f, __uint_as_float(ov[2 * e + 1]) * f);
-          if ((reinterpret_cast<uintptr_t>(op) & 15) == 0) {
-#pragma unroll
-            for (int e = 0; e < 16; e += 4) *reinterpret_cast<uint4*>(op + 2 * e) = make_uint4(w[e], w[e + 1], w[e + 2], w[e + 3]);
-          } else {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) op[2 * e] = uint16_t(w[e]), op[2 * e + 1] = uint16_t(w[e] >> 16);
+          for (int e = 0; e < 32; ++e) op[e] = f32_to_bf16(__uint_as_float(ov[e]) * f);
+        }
+        if (wide) {
+          __syncwarp();
+          constexpr int kLanes = D / 8, kPer = 32 / kLanes;
+#pragma unroll 8
+          for (int i = 0; i < kLanes; ++i) {
+            const int in = i * kPer + lane / kLanes, at_row = (warp & 3) * 32 + in, piece = lane % kLanes;
+            const uint64_t to = __shfl_sync(kFull, own, in);
+            uint4 w;
+            asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+                         : "r"(qs + t * C::kQBytes + (piece >> 3) * 16384 + at_row * 128 + (((piece & 7) ^ (at_row & 7)) << 4))
+                         : "memory");
+            if (to) *(reinterpret_cast<uint4*>(to) + piece) = w;
           }
         }
         if (live) {

@@ -498,6 +498,29 @@ def test_many_requests_share_out_evenly(nq, B, heads, kv_heads, D, least, most, 
         assert torch.equal(again, out) and torch.equal(lse_again, lse)
 
 
+@pytest.mark.parametrize("heads,kv_heads,D,window", [(16, 4, 64, 0), (16, 4, 128, 150), (8, 4, 256, 0), (12, 4, 128, 0)])
+def test_more_tiles_than_multiprocessors(nq, heads, kv_heads, D, window):
+    """Prompts and chunks of every length, some of no token, in one call: a CTA takes several tiles of them."""
+    rng = np.random.default_rng(D + heads)
+    n = [int(x) for x in rng.integers(0, 400, 60)]
+    n[3], n[7], n[8], n[59] = 0, 0, 129, 0
+    t = [x + int(y) for x, y in zip(n, rng.integers(0, 300, 60))]
+    s = make(nq, n, t, heads, kv_heads, D, 16, seed=18, tail=3)
+    ws = torch.zeros(nq.ATTENTION_WORKSPACE_BYTES, dtype=torch.uint8, device="cuda")
+    out, lse = check(nq, s, window=window, workspace=ws)
+    args = (s["cache"], s["table"], s["kv_lens"], s["cu"], s["gk"], s["gv"])
+    again = torch.empty_like(out)
+    graph, stream = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(graph, stream=stream):
+        for _ in range(2):
+            nq.nq_attention_nvfp4_kv(s["q"], *args, window=window, out=again, workspace=ws, flags=nq.FLAG_PDL)
+    for _ in range(3):
+        again.fill_(123.0)
+        graph.replay()
+        assert torch.equal(again, out)
+    nq.nq_check_device_errors()
+
+
 def test_many_requests_captured_with_a_shared_workspace(nq):
     s = many(nq, 400, 8, 2, 128, 1, 500, seed=16)
     ws = torch.zeros(nq.ATTENTION_WORKSPACE_BYTES, dtype=torch.uint8, device="cuda")
