@@ -22,15 +22,16 @@
 //
 // A warp finds the next item while this one is worked on, the producers go on to
 // its keys while the last blocks are multiplied, and the barriers count on, so that
-// between items only the output and the queries stand still.  (With a CTA per item,
-// 16 chunks of 512 behind 1536 tokens, 8 kv heads: of 128 332 us, now 315; of 256
-// 385, now 358; of 64 506, now 465.)  A prompt of 8192, 32/8 heads of 128: 552 us, 996
-// TFLOP/s, 0.62 of the measured product rate; a block of 128 keys takes the CTA
-// about 4400 cycles, of which products, exponentials and the conversion's way
-// through shared memory are about 2000 each and overlap in part.  One tile alone
-// (an item of at most 128 rows) still takes 3900 a block; with its keys shared out
-// between two tiles of the same rows, 24 x 64 rows over 4096 keys took 133 us
-// instead of 141, but items of two tiles lost 3 to 7 %.  Items are claimed when
+// between items only the output and the queries stand still.  Measured with 16 chunks
+// of 512 behind 1536 tokens, 8 kv heads of 128 / 256 / 64: a CTA per item 332 / 385 /
+// 506 us, items in turn 315 / 358 / 465, query rows loaded in one go 274 / 287 / 430,
+// rows loaded and stored side by side 274 / 279 / 436.  A prompt of 8192, 32/8 heads
+// of 128, alone: 510 us, 1078 TFLOP/s, 0.67 of the measured product rate; a block of 128
+// keys takes the CTA about 4100 cycles, of which products, exponentials and the
+// conversion's way through shared memory are about 2000 each and overlap in part.
+// An item of at most 128 rows takes almost as long; with its keys shared out between
+// two tiles of the same rows, 24 x 64 rows over 4096 keys gained 6 %, but items of
+// two tiles lost 3 to 7 %.  Items are claimed when
 // five blocks of the item before are left: earlier, the last items went to CTAs
 // that were not the first to be free (256 items of 33 blocks: 252 us, now 168).
 //

@@ -239,12 +239,12 @@ nq_status nq_attention_nvfp4_kv(const void* q, int64_t ld_q_token, int64_t ld_q_
   const int64_t segments = (T * a.group / (8 * n_tiles) + B) * kv_heads;
   const bool few = segments <= grid / 2;
   // Rows kernel / 128-row tiles, 8 kv heads, us:
-  //                             d = 64           d = 128                        d = 256
-  //   24 requests of 4096 keys  64 rows  83/116  48 rows 122/135, 64 rows 149/135  24 rows 150/182, 32 rows 191/184
-  //   200 requests of 700 keys  64 rows 144/203  48 rows 173/270, 64 rows 220/277  24 rows 212/371, 32 rows 273/387
-  //   2 requests of 8192 (few)  32 rows  24/31   32 rows  28/39,  48 rows  37/41   24 rows  45/51,  32 rows  45/51
-  //   1 request of 65536 (few)  32 rows  39/64   32 rows  61/78,  48 rows  86/78   16 rows  66/100, 24 rows 111/100
-  const int64_t most = d == 256 ? 24 : (few ? 32 : (d == 128 ? 48 : 64));
+  //                             d = 64            d = 128                          d = 256
+  //   24 requests of 4096 keys  64 rows  84/115   48 rows 123/132, 64 rows 150/133   24 rows 152/166, 32 rows 190/168
+  //   200 requests of 700 keys  64 rows 143/164   48 rows 174/199, 64 rows 221/201   24 rows 211/231, 32 rows 272/238
+  //   2 requests of 8192 (few)  32 rows  23/31    32 rows  29/39                     16 rows  35/43,  24 rows  45/43
+  //   1 request of 65536 (few)  32 rows  39/66    32 rows  61/78,  48 rows  86/78    16 rows  66/92,  24 rows 111/96
+  const int64_t most = d == 256 ? (few ? 16 : 24) : (few ? 32 : (d == 128 ? 48 : 64));
   if (rows > most) {
     const nq::AttnTiles t = nq::attn_tiles(d);
     if (!nq::host::allow_smem(t.kernel, t.smem))
