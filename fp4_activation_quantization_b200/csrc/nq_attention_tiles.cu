@@ -27,8 +27,9 @@
 // 506 us, items in turn 315 / 358 / 465, query rows loaded in one go 274 / 287 / 430,
 // rows loaded and stored side by side 274 / 279 / 436.  A prompt of 8192, 32/8 heads
 // of 128, alone: 510 us, 1078 TFLOP/s, 0.67 of the measured product rate; a block of 128
-// keys takes the CTA about 4100 cycles, of which products, exponentials and the
-// conversion's way through shared memory are about 2000 each and overlap in part.
+// keys takes the CTA about 4100 cycles; products and exponentials are about 2100 each
+// (tensor pipe 53 %, exponential unit 51 % busy), and a tile's own chain, S to maximum
+// to exponentials to P V to the next S, is what the step waits for.
 // An item of at most 128 rows takes almost as long; with its keys shared out between
 // two tiles of the same rows, 24 x 64 rows over 4096 keys gained 6 %, but items of
 // two tiles lost 3 to 7 %.  Items are claimed when
