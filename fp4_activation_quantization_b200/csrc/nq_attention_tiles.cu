@@ -91,7 +91,7 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
 // a wait that may take as long as an item, so it leaves the issue slots to others.
 template <bool NAP>
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* gave_up) {
-  for (int i = 0; i < (1 << 22); ++i) {
+  for (int i = 0; i < (NAP ? 1 << 26 : 1 << 22); ++i) {
     if (mbar_try(bar, parity)) return true;
     if ((i & 1023) == 1023 && *gave_up) return false;
     if (NAP && i > 8) __nanosleep(200);

@@ -107,7 +107,7 @@ constexpr int kAttnTilesThreads = 512;
 struct AttnTiles {
   const void* kernel;
   const void* join;  // 256 threads, 8 rows a CTA; only after a kernel with splits > 1
-  int rows;          // of a CTA
+  int rows;          // of an item
   size_t smem;
 };
 AttnTiles attn_tiles(int d);
