@@ -876,11 +876,16 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
         const uint32_t both = uint32_t(tiles) | 1u;  // bit t: tile t has rows
         const uint32_t q_now = q_par;
         q_par ^= both;
-        if (n == 0) continue;
         auto wait_q = [&](int t) {
           ok = ok && mbar_wait_warp(q_full(t), (q_now >> t) & 1, gave_up);
           fence_after();
         };
+        if (n == 0) {
+          // No phase of q_full is passed by: the softmax warps may be an item behind, and the parity of the next
+          // item's phase is that of the one before this.
+          for (int t = 0; t < tiles; ++t) wait_q(t);
+          continue;
+        }
         wait_slot(q);
         if constexpr (C::kTiles == 2) {
           for (int t = 0; t < tiles && ok; ++t) {
