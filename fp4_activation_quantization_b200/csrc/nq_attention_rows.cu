@@ -2,7 +2,7 @@
 // (single tokens, draft verification): each warp streams atoms of 16 tokens
 // through matrix products whose fragments are the cache's own byte order.
 //
-//   s_j = c <q, k'_j>,  m = max s_j,  p_j = 2^(s_j - m),  l = sum p_j,
+//   s_j = c <q, k'_j>,  m = max s_j - 7,  p_j = 2^(s_j - m),  l = sum p_j,
 //   o = g_v / l * sum p_j v'_j,  lse = ln 2 (m + log2 l),
 // with k', v' = e2m1 * e4m3 and c = scale * log2(e) * g_k.
 //
@@ -10,10 +10,13 @@
 // 2688], so they are exact in f16.  A query row is scaled by a power of two to
 // a largest magnitude in [2^14, 2^15): its bf16 values are then exact in f16
 // down to 2^-28 of the row's largest.  Products accumulate in float32.  p is
-// rounded to f16 (half a step is 2^-11 of it, an eighth of the bf16 output's);
-// l sums the float32 values.  The running maximum is only raised when a score
-// exceeds it by more than 2^8: p stays below 2^9, far inside f16's range, and
-// the accumulators are rescaled once or twice per row instead of at every atom.
+// rounded to f16: half a step is 2^-11 of it, an eighth of the bf16 output's,
+// and 2^-32 of the row's largest where that is more (f16's subnormal numbers),
+// which n keys can lose of a sum of p once each, less than the 2^-24 of the
+// sum that each of n additions in float32 may lose.  l sums the float32
+// values.  m lies 2^7 below the running maximum, and that is only raised when
+// a score exceeds it by more than 2^8: p stays at or below 2^15, and the
+// accumulators are rescaled once or twice per row instead of at every atom.
 //
 // Work.  S^T = K' q^T and O^T = V'^T P^T put the 16 tokens (or dimensions) on
 // the 16-row side of the product and up to 8 rows of a (request, kv head) on
@@ -45,7 +48,6 @@ namespace nq {
 namespace {
 
 constexpr int kWalkWarps = 4, kChunkWarps = 8;
-constexpr float kRaise = 8.0f;      // log2 by which a score may exceed the running maximum
 constexpr float kLowest = -3.0e38f; // the maximum of no scores: below every finite one, and 0 * 2^(kLowest - kLowest) is 0
 
 constexpr int stages_of(int d) { return d == 64 ? 3 : 2; }  // pairs of atoms
@@ -164,9 +166,6 @@ __device__ __forceinline__ void store_pair(uint16_t* op, float x0, float x1) {
   }
 }
 __device__ __forceinline__ float out_factor(float sum, float gv) { return sum > 0.0f || sum != sum ? gv / sum : 0.0f; }
-__device__ __forceinline__ float lse_of(float top, float sum) {
-  return sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
-}
 
 // Joins n parts of a tile (part p at slot(p)), in order, with THREADS threads of a
 // CTA, and writes the rows out.  Weights first, then the rows in independent
@@ -649,7 +648,7 @@ __global__ void __launch_bounds__((WALK ? kWalkWarps : kChunkWarps) * 32,
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int x = 0; x < 4; ++x) raise |= __fmaf_rn(sc[n][nt][x], cs[nt][x & 1], -m[nt][x & 1]) > kRaise;
+          for (int x = 0; x < 4; ++x) raise |= __fmaf_rn(sc[n][nt][x], cs[nt][x & 1], -m[nt][x & 1]) > kHeadroom + kRaise;
       if (__any_sync(kFull, raise)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -659,8 +658,8 @@ __global__ void __launch_bounds__((WALK ? kWalkWarps : kChunkWarps) * 32,
             if (N == 2) top = fmaxf(top, fmaxf(sc[N - 1][nt][y], sc[N - 1][nt][y + 2]));
 #pragma unroll
             for (int w = 4; w < 32; w <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, w));
-            if (__fmaf_rn(top, cs[nt][y], -m[nt][y]) > kRaise) {  // a row's results do not depend on its neighbours'
-              top *= cs[nt][y];
+            if (__fmaf_rn(top, cs[nt][y], -m[nt][y]) > kHeadroom + kRaise) {  // a row's results do not depend on its neighbours'
+              top = __fmaf_rn(top, cs[nt][y], -kHeadroom);
               const float f = ex2(m[nt][y] - top);
               m[nt][y] = top;
               l[nt][y] *= f;

@@ -3,7 +3,7 @@
 //
 // The mathematics and the numerics are those of nq_attention_rows.cu: k' and v'
 // exact in f16, query rows scaled by a power of two, float32 accumulation, f16
-// weights, the running maximum raised only by more than 2^8.
+// weights that reach up to 2^15, the running maximum raised only by more than 2^8.
 //
 // One CTA an SM takes items in turn: NS tiles of 128 (token, head of the group)
 // rows of one request and kv head.  It walks an item's keys in blocks of 128:
@@ -47,7 +47,6 @@ namespace {
 constexpr int kThreads = kAttnTilesThreads;
 constexpr int kBlock = 128;  // keys of a block
 constexpr int kAtoms = kBlock / 16;
-constexpr float kRaise = 8.0f;
 constexpr int kBad = 8;  // ring of the blocks' missing-atom masks
 
 template <int D>
@@ -540,7 +539,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
           for (int e = 2; e < 32; e += 2)
             tops[y] = fmax3(tops[y], __uint_as_float(sv[32 * y + e]), __uint_as_float(sv[32 * y + e + 1]));
         }
-        const float top = fmaxf(fmax3(tops[0], tops[1], tops[2]), tops[3]) * c;
+        const float top = __fmaf_rn(fmaxf(fmax3(tops[0], tops[1], tops[2]), tops[3]), c, -kHeadroom);
         const bool raise = top > m + kRaise;
         if (__any_sync(kFull, raise)) {
           const float f = raise ? ex2(m - top) : 1.0f;
@@ -662,7 +661,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
           if (part != nullptr)
             *reinterpret_cast<float2*>(part - row * D + C::kRows * D + 2 * row) = make_float2(m, l);
           else if (a.lse != nullptr)
-            a.lse[at * a.ld_lse + head] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+            a.lse[at * a.ld_lse + head] = lse_of(m, l);
         }
       }
     }
@@ -998,7 +997,7 @@ __global__ void __launch_bounds__(256) join_kernel(const AttnArgs a) {
   for (int i = 0; i < D / 32; ++i)
     a.out[at * a.ld_ot + int64_t(head) * a.ld_oh + 32 * i + lane] = f32_to_bf16(o[i] * f);
   if (lane == 0 && a.lse != nullptr)
-    a.lse[at * a.ld_lse + head] = l == 0.0f ? -INFINITY : (top + log2f(l)) * 0.6931471805599453f;
+    a.lse[at * a.ld_lse + head] = lse_of(top, l);
 }
 
 }  // namespace

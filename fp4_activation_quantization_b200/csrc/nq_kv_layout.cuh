@@ -63,6 +63,15 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t c) {
   asm("{\n\t.reg .b16 c2;\n\tcvt.u16.u32 c2, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, c2;\n\t}" : "=r"(h) : "r"(c));
   return h;
 }
+// Softmax weights 2^(s - m) are rounded to f16.  m lies kHeadroom below a score that was the running maximum and is
+// raised once a score exceeds that one by more than kRaise (both log2): weights reach 2^15, in f16's range, and the
+// largest of a row is 2^7 at least, so f16's smallest half step, 2^-25, is 2^-32 of it.  Without the headroom a long,
+// flat tail 2^25 below one early peak was lost whole.
+constexpr float kHeadroom = 7.0f, kRaise = 8.0f;
+// log sum exp of the scores: from m and the sum of 2^(s - m); exact in m's part whatever m was rounded to.
+__device__ __forceinline__ float lse_of(float m, float sum) {
+  return sum == 0.0f ? -INFINITY : ((m + kHeadroom) + log2f(sum * 0.0078125f)) * 0.6931471805599453f;
+}
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   uint32_t d;
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));

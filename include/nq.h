@@ -451,7 +451,8 @@ nq_status nq_kv_gather_nvfp4(const void* cache, int64_t page_stride, int64_t num
  *     zero-filled before its first use; every call leaves it ready for the next.
  *     Calls that may run at the same time need one each.
  * Sums, softmax statistics and accumulators are float32; softmax weights are
- * rounded to f16 before they meet the values.  Results do not depend on timing.
+ * rounded to f16 before they meet the values (an error of 2^-11 of the weight or
+ * 2^-32 of the row's largest, whichever is more).  Results do not depend on timing.
  * A page outside the cache is skipped, its keys count as out of sight, and bit 2
  * of the device error word is set.  Memory behind a request's last key is never
  * used, whatever it holds.  table_width * page_size <= 2^30; a longer kv_len is

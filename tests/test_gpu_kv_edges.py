@@ -1,7 +1,9 @@
 """GPU tests of the 4-bit key/value cache at its edges."""
+import numpy as np
 import pytest
 import torch
 
+import kv_helpers as K
 from test_gpu_kv import check, make, nq  # noqa: F401  (fixture)
 
 pytestmark = pytest.mark.gpu
@@ -9,6 +11,11 @@ pytestmark = pytest.mark.gpu
 
 def call(nq, s, **more):
     return nq.nq_attention_nvfp4_kv(s["q"], s["cache"], s["table"], s["kv_lens"], s["cu"], s["gk"], s["gv"], **more)
+
+
+# Rows and keys of a batch that takes each form of the kernels: one chunk a CTA, a share a warp, 128-row tiles.
+FORMS = {"chunks": ([1] * 3, [700, 40, 300]), "walk": ([1] * 300, [100 + 7 * (i % 50) for i in range(300)]),
+         "tiles": ([150, 200], [300, 200])}
 
 
 # ------------------------------------------------------------------------------------------- tiles without keys ----
@@ -23,3 +30,39 @@ def test_tiles_without_keys_between_others(nq, D, pattern):
     for _ in range(20):  # which CTA takes which tile differs from run to run
         again, lse_again = call(nq, s, workspace=ws, want_lse=True)
         assert torch.equal(again, out) and torch.equal(lse_again, lse)
+
+
+# --------------------------------------------------------------------------------- weights far below the largest ----
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("n,t", [*FORMS.values(), ([1] * 2, [131073, 5000]), ([150, 90], [9000, 4000])])
+def test_a_flat_tail_behind_one_early_peak(nq, n, t, D):
+    """The first key is e^17.4 = 2^25.1 times as heavy as any other and its value is zero: the output is the tail's."""
+    page = 64
+    s = make(nq, n, t, 4, 1, D, page, seed=D)
+    first = torch.cat([(torch.arange(x, device="cuda") == 0) for x in t])
+    k = torch.zeros((sum(t), 1, D), device="cuda")
+    k[first, :, 0] = 1.0
+    v = torch.ones_like(k)
+    v[first] = 0.0
+    slots = torch.cat([s["table"][b].long()[torch.arange(x, device="cuda") // page] * page + torch.arange(x, device="cuda") % page
+                       for b, x in enumerate(t)])
+    nq.nq_kv_append_nvfp4(k.bfloat16(), v.bfloat16(), slots, s["cache"], s["gk"], s["gv"])
+    kd, vd = K.decode(s["cache"][s["table"][0, 0]][None], D, page)
+    key, value = float(kd[0, 0, 0, 0]) * float(s["gk"]), float(vd[0, 1, 0, 0]) * float(s["gv"])
+    s["q"].zero_()
+    s["q"][..., 0] = 1.0
+    scale = float(np.float32(17.4 / key))
+    out, lse = call(nq, s, scale=scale, want_lse=True)
+    tail = torch.cat([torch.arange(x - m, x, device="cuda") for m, x in zip(n, t)]).double()  # keys behind the first
+    peak = scale * key
+    w = np.exp(-peak)
+    want = (value * tail * w / (1 + tail * w))[:, None, None]
+    # As for any row (a weight's f16 half step and its exponent's float32 errors, the sums' over `tail` keys, the output's
+    # bf16 half step); f16's smallest half step, 2^-25, beside a largest weight of 2^7 at least, for each key of the tail.
+    eps = D * 2.0**-23 * peak + 2 * 2.0**-23 * peak + 2.0**-22
+    err = want * (2.0**-11 + 2 * eps + 2 * (tail[:, None, None] + 1) * 2.0**-23) + 2.0**-32 * value * tail[:, None, None]
+    d = (out.double() - want).abs()
+    assert bool((d <= 2.0**-8 * (want + err) + err).all()), float((d / want.clamp(min=1e-300)).max())
+    want = peak + torch.log1p(tail * w)[:, None]
+    assert bool(((lse.double() - want).abs() <= eps + (tail[:, None] + 1) * 2.0**-23 + 2.0**-22 * (1 + want)).all())
+    nq.nq_check_device_errors()
