@@ -387,15 +387,16 @@ int64_t nq_kv_page_bytes(int32_t kv_heads, int32_t d, int32_t page_size);
  *     ceil(cached / page_size) to ceil((cached + new) / page_size) - 1, taking
  *     pages in request order from free_pages int32 [n_free] at entry
  *     free_head[0], and leaves every other column as it was.
- *   free_head_out int32 [1]  free_head[0] + the pages taken.  May equal
- *     free_head: a replayed graph then takes further pages each time.
+ *   free_head_out int32 [1]  free_head[0] + the pages taken, n_free at most.  May
+ *     equal free_head: a replayed graph then takes further pages each time.
  *   cu_q int32 [B + 1]  first token row of each request and their total;
  *   kv_lens int32 [B]   cached + new;
  *   positions int32 [T], slots int64 [T]  of the tokens, request after request;
  *     rows behind the last token (a padded batch) get -1.
  * A request that outgrows its table row, tokens past T and pages past the free
- * list's end (table entry -1, slot -1) set bit 3 of the device error word;
- * lengths are then cut to the table's width and cu_q to T.  Negative lengths
+ * list's end (slot -1; table entry -1, as far as the first 2^31 - 1 pages go) set
+ * bit 3 of the device error word; lengths are then cut to the table's width and
+ * cu_q to T, whatever the lengths sum up to.  Negative lengths
  * count as 0 and set the same bit.  Integers only: results are exact.
  * B <= NQ_KV_MAX_REQUESTS; table_width * page_size <= 2^30.  flags:
  * NQ_FLAG_PDL.

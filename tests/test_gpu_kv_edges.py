@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import kv_helpers as K
-from test_gpu_kv import check, make, nq  # noqa: F401  (fixture)
+from test_gpu_kv import check, i32, make, nq  # noqa: F401  (fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -66,3 +66,48 @@ def test_a_flat_tail_behind_one_early_peak(nq, n, t, D):
     want = peak + torch.log1p(tail * w)[:, None]
     assert bool(((lse.double() - want).abs() <= eps + (tail[:, None] + 1) * 2.0**-23 + 2.0**-22 * (1 + want)).all())
     nq.nq_check_device_errors()
+
+
+# ----------------------------------------------------------------------------------------- plans that do not fit ----
+def test_a_plan_of_more_than_32_bits_of_tokens_is_cut(nq):
+    B, T, page = 4, 8, 128
+    width = (1 << 30) // page
+    table = torch.full((B, width), -7, dtype=torch.int32, device="cuda")
+    zero, head = i32([0] * B), i32([1])
+    out = nq.nq_kv_plan(zero, i32([1 << 30] * B), table, i32([4, 5, 6]), head, T, page, free_head_out=head)
+    with pytest.raises(nq.NQError, match="bit 3"):
+        nq.nq_check_device_errors()
+    cu, kv, pos, slots, _ = (x.tolist() for x in out)
+    assert cu == [0, T, T, T, T] and kv == [1 << 30] * B
+    assert pos == list(range(T)) and slots == list(range(5 * page, 5 * page + T))
+    assert int(head) == 3  # the pages that the list still held
+    assert table[0, :3].tolist() == [5, 6, -1] and bool((table[1:] == -1).all())
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+def test_a_plan_takes_the_pages_that_are_left(nq, in_place):
+    table = torch.full((3, 4), -7, dtype=torch.int32, device="cuda")
+    free, head = i32([10, 11, 12]), i32([1])
+    for step, (want, left) in enumerate([([[11, -7], [12, -1], [-1, -7]], 3), ([[11, -1], [12, -1], [-1, -1]], 3)]):
+        out = nq.nq_kv_plan(i32([16 * step, 32 * step, 16 * step]), i32([16, 32 if step == 0 else 0, 16]), table, free, head,
+                            64 if step == 0 else 32, 16, free_head_out=head if in_place else None)
+        with pytest.raises(nq.NQError, match="bit 3"):
+            nq.nq_check_device_errors()
+        head = out[4]
+        assert int(head) == left and table[:, :2].tolist() == want and bool((table[:, 2:] == -7).all())
+
+
+def test_a_plan_of_more_than_32_bits_of_pages_is_cut(nq):
+    """66 requests of 2^26 pages each."""
+    B, T, page = 66, 5, 16
+    width = (1 << 30) // page
+    table = torch.empty((B, width), dtype=torch.int32, device="cuda")
+    table[-1] = -7
+    out = nq.nq_kv_plan(i32([0] * B), i32([1 << 30] * B), table, i32([4, 5, 6]), i32([0]), T, page)
+    with pytest.raises(nq.NQError, match="bit 3"):
+        nq.nq_check_device_errors()
+    cu, kv, pos, slots, head = (x.tolist() for x in out)
+    assert cu == [0] + [T] * B and kv == [1 << 30] * B and head == [3]
+    assert pos == list(range(T)) and slots == list(range(4 * page, 4 * page + T))
+    assert table[0, :4].tolist() == [4, 5, 6, -1] and bool((table[:31, 3:] == -1).all())
+    assert bool((table[-1] == -7).all())  # past the 2^31 - 1 pages that a plan lays out
