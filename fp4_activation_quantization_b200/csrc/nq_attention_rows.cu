@@ -808,6 +808,11 @@ __global__ void __launch_bounds__((WALK ? kWalkWarps : kChunkWarps) * 32,
       for (int y = 0; y < 2; ++y)
 #pragma unroll
         for (int w = 4; w < 32; w <<= 1) l[nt][y] += __shfl_xor_sync(kFull, l[nt][y], w);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int y = 0; y < 2; ++y)
+        if (l[nt][y] > 0.0f) l[nt][y] += nan_of(a.scale_log2 * gk);
     if constexpr (WALK) {
       if (seg0 >= u0 && seg0 + units <= u1) {
 #pragma unroll

@@ -596,7 +596,8 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
         done ^= 1u << 31;
         fence_after();
       }
-      const float l = (l2[0].x + l2[0].y) + (l2[1].x + l2[1].y);
+      float l = (l2[0].x + l2[0].y) + (l2[1].x + l2[1].y);
+      if (l > 0.0f) l += nan_of(a.scale_log2 * __ldg(a.k_scale));
       const int x = it.row0 + row, token = x / a.group, head = it.head * a.group + x - token * a.group;
       const int64_t at = it.q0 + token;
       float* part = nullptr;

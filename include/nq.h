@@ -445,7 +445,7 @@ nq_status nq_kv_gather_nvfp4(const void* cache, int64_t page_stride, int64_t num
  *     NQ_FLAG_NONCAUSAL), and with window > 0 j > p - window.
  *   s_j = softmax_scale * k_scale[0] * <q, e2m1 * sf of key j>, p = softmax(s),
  *   out = RN_bf16(v_scale[0] * sum_j p_j (e2m1 * sf of value j)); a row without
- *     keys gives zeros.
+ *     keys gives zeros.  A scale that is NaN makes NaN of every row with keys.
  *   lse float32 [T, ld_lse] (ld_lse >= heads) log sum_j exp(s_j), -inf for a row
  *     without keys; or NULL.
  *   workspace: NQ_ATTENTION_WORKSPACE_BYTES of device memory, 16-byte aligned,

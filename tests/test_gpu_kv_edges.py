@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import kv_helpers as K
-from test_gpu_kv import check, i32, make, nq  # noqa: F401  (fixture)
+from test_gpu_kv import check, f32, i32, make, nq  # noqa: F401  (fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -111,3 +111,22 @@ def test_a_plan_of_more_than_32_bits_of_pages_is_cut(nq):
     assert pos == list(range(T)) and slots == list(range(4 * page, 4 * page + T))
     assert table[0, :4].tolist() == [4, 5, 6, -1] and bool((table[:31, 3:] == -1).all())
     assert bool((table[-1] == -7).all())  # past the 2^31 - 1 pages that a plan lays out
+
+
+# -------------------------------------------------------------------------------- scales and queries at their ends ----
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("n,t", [([1] * 3, [700, 0, 300]), ([1] * 300, [(7 * i) % 350 for i in range(300)]),
+                                 ([150, 200], [300, 120]), ([1], [20000]), ([150], [9000])])
+def test_a_nan_scale_is_seen(nq, n, t, D):
+    s = make(nq, n, t, 8, 2, D, 16, seed=D)
+    keys = torch.cat([torch.arange(x - m, x, device="cuda") >= 0 for m, x in zip(n, t)])
+    nan = f32(float("nan"))
+    for gk, gv in ((nan, s["gv"]), (s["gk"], nan)):
+        out, lse = call(nq, {**s, "gk": gk, "gv": gv}, want_lse=True)
+        assert bool(out[keys].isnan().all()) and not out[~keys].any()
+        assert bool(torch.isneginf(lse[~keys]).all())
+        if gk is nan:
+            assert bool(lse[keys].isnan().all())
+        else:
+            assert bool(lse[keys].isfinite().all())
+    nq.nq_check_device_errors()
