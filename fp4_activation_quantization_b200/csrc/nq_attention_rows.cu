@@ -9,7 +9,8 @@
 // Numerics.  k' and v' have at most six significant bits and lie in [2^-10,
 // 2688], so they are exact in f16.  A query row is scaled by a power of two to
 // a largest magnitude in [2^14, 2^15): its bf16 values are then exact in f16
-// down to 2^-28 of the row's largest.  Products accumulate in float32.  p is
+// down to 2^-28 of the row's largest (a row whose largest lies below 2^-112, to
+// one below 2^14, and exact down to 2^-126 * 2^-24).  Products accumulate in float32.  p is
 // rounded to f16: half a step is 2^-11 of it, an eighth of the bf16 output's,
 // and 2^-32 of the row's largest where that is more (f16's subnormal numbers),
 // which n keys can lose of a sum of p once each, less than the 2^-24 of the
@@ -553,7 +554,7 @@ __global__ void __launch_bounds__((WALK ? kWalkWarps : kChunkWarps) * 32,
       amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 1));
       amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 2));
       const int e = int(__float_as_uint(amax) >> 23) - 127;
-      const int k = (amax == 0.0f || e > 127) ? 0 : min(14 - e, 100);
+      const int k = (amax == 0.0f || e > 127) ? 0 : min(14 - e, kMostPower);
       const float factor = a.scale_log2 * gk;
       const float up = copysignf(__uint_as_float(uint32_t(k + 127) << 23), factor);
       // At least the smallest normal number: 0 would make NaN of a masked key's -inf.

@@ -441,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
         const float factor = a.scale_log2 * __ldg(a.k_scale);
         auto power = [](float amax) {  // of two, to which the row's largest is scaled
           const int e = int(__float_as_uint(amax) >> 23) - 127;
-          return amax == 0.0f || e > 127 ? 0 : min(14 - e, 100);
+          return amax == 0.0f || e > 127 ? 0 : min(14 - e, kMostPower);
         };
         const uint32_t q_tile = qs + t * C::kQBytes;
         float mine = 0.0f;  // this thread's row's largest

@@ -72,6 +72,8 @@ constexpr float kHeadroom = 7.0f, kRaise = 8.0f;
 __device__ __forceinline__ float lse_of(float m, float sum) {
   return sum == 0.0f ? -INFINITY : ((m + kHeadroom) + log2f(sum * 0.0078125f)) * 0.6931471805599453f;
 }
+// The largest power of two by which a query row is scaled: its inverse, too, is a normal number.
+constexpr int kMostPower = 126;
 // 0, or NaN for a score factor that is none: added to the sum of a row that has keys, as its c hides a NaN.
 __device__ __forceinline__ float nan_of(float factor) { return factor - factor; }
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {

@@ -130,3 +130,15 @@ def test_a_nan_scale_is_seen(nq, n, t, D):
         else:
             assert bool(lse[keys].isfinite().all())
     nq.nq_check_device_errors()
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("power", [100, 120, 130])
+def test_small_queries_of_large_keys(nq, form, D, power):
+    """Queries down to bf16's subnormal numbers under a key scale that is as large: scores of ordinary size."""
+    s = make(nq, *FORMS[form], 8, 2, D, 16, seed=power)
+    s["q"] = (s["q"].double() * 2.0**-power).bfloat16()
+    assert bool((s["q"] != 0).any())
+    s["gk"] = (s["gk"].double() * 2.0**power).float()
+    check(nq, s)
