@@ -529,6 +529,17 @@ def _launch(dev: int, name: str, args, stream) -> None:
         raise NQError(status, name)
 
 
+def _new(make, shape, dtype, device, stream):
+    """A tensor made by ``make`` (torch.empty, torch.zeros) on the stream that the call runs on: filled, and given back,
+    in its order."""
+    if stream is None:
+        return make(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):  # a handle; 0 is the default stream, of which ExternalStream makes a new one
+        stream = torch.cuda.ExternalStream(int(stream), device) if int(stream) else torch.cuda.default_stream(device)
+    with torch.cuda.stream(stream):
+        return make(shape, dtype=dtype, device=device)
+
+
 def _wrong(dev, **want) -> None:
     """Raise ValueError for the first tensor that is not (tensor, dtype, shape, contiguous); None in a shape: any."""
     for name, (t, dtype, shape, contiguous) in want.items():
@@ -743,9 +754,7 @@ def nq_attention_nvfp4_kv(q, cache, block_table, kv_lens, cu_q, k_scale, v_scale
         lse_p, ld_lse = lse.data_ptr(), (ld_lse if T > 1 else max(ld_lse, heads))
     _need(0 <= window < 1 << 31, "window must lie in 0 .. 2^31 - 1")
     if workspace is None:
-        on = stream if stream is None or isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(stream, q.device)
-        with torch.cuda.stream(on):  # zeroed, and given back, in the order of the stream that the call runs on
-            workspace = torch.zeros(ATTENTION_WORKSPACE_BYTES, dtype=_u8, device=q.device)
+        workspace = _new(torch.zeros, ATTENTION_WORKSPACE_BYTES, _u8, q.device, stream)
     elif _device_of(workspace) != dev or workspace.dtype is not _u8 or workspace.dim() != 1 or not workspace.is_contiguous():
         _wrong(dev, workspace=(workspace, _u8, (None,), True))
     _launch(dev, "nq_attention_nvfp4_kv",

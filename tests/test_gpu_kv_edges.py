@@ -142,3 +142,25 @@ def test_small_queries_of_large_keys(nq, form, D, power):
     assert bool((s["q"] != 0).any())
     s["gk"] = (s["gk"].double() * 2.0**power).float()
     check(nq, s)
+
+
+# ------------------------------------------------------------------------------------------------- other streams ----
+def test_a_workspace_of_the_default_stream(nq, monkeypatch):
+    """Handle 0 is the default stream: the workspace is zeroed there, in front of the kernel, whatever stream is current."""
+    s = make(nq, *FORMS["walk"], 8, 2, 128, 16, seed=19)
+    want, want_lse = call(nq, s, want_lse=True)
+    torch.cuda.synchronize()
+    made, zeros = [], torch.zeros
+
+    def noted(*args, **kw):
+        made.append(torch.cuda.current_stream().cuda_stream)
+        return zeros(*args, **kw)
+    side = torch.cuda.Stream()
+    monkeypatch.setattr(torch, "zeros", noted)
+    for current in (torch.cuda.default_stream(), side):
+        for handle in (0, torch.cuda.default_stream(), side, side.cuda_stream):
+            with torch.cuda.stream(current):
+                out, lse = call(nq, s, out=torch.empty_like(want), lse=torch.empty_like(want_lse), stream=handle)
+            assert made.pop() == (side.cuda_stream if handle in (side, side.cuda_stream) else 0) and not made
+            torch.cuda.synchronize()
+            assert torch.equal(out, want) and torch.equal(lse, want_lse)
