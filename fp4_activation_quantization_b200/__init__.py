@@ -4,8 +4,12 @@ A thin ctypes binding over ``libnq.so`` (see ``include/nq.h`` for the
 contract of every call).  This module only marshals arguments: it checks
 tensor dtypes / devices / layouts, allocates outputs with torch when the
 caller does not pass them, and forwards raw device pointers, strides and the
-current CUDA stream.  Every arithmetic step runs in the library's CUDA
-kernels; there is no CPU or PyTorch fallback.  The library is loaded on first
+current CUDA stream, or the one given as ``stream=``, on which every tensor
+passed in has to be ready.  (Then the key/value cache calls make their results
+on that stream; the norm and quantization calls take theirs from the current
+stream's memory, so pass outputs of your own or order the two streams.)  Every
+arithmetic step runs in the library's CUDA kernels; there is no CPU or PyTorch
+fallback.  The library is loaded on first
 use, and that use raises ImportError when it has not been built
 (``python -m fp4_activation_quantization_b200.build``).
 
@@ -502,6 +506,8 @@ def nq_fused_add_rmsnorm_quant_fp8_moe(x, gamma, dest, rows: int, eps: float = 1
 
 
 # ------------------------------------------------- the 4-bit key/value cache ----
+# ``stream=``: the tensors passed in have to be ready on that stream; results that
+# the call makes belong to it, as if it were the current one.
 def kv_cache_shape(num_pages: int, kv_heads: int, head_dim: int, page_size: int):
     """Shape of a uint8 cache tensor: [pages, kv heads, page_size * head_dim * 9 / 8]."""
     return num_pages, kv_heads, page_size * head_dim * 9 // 8
@@ -531,7 +537,7 @@ def _launch(dev: int, name: str, args, stream) -> None:
 
 def _new(make, shape, dtype, device, stream):
     """A tensor made by ``make`` (torch.empty, torch.zeros) on the stream that the call runs on: filled, and given back,
-    in its order."""
+    in its order (what another stream had before, that stream may still have to write)."""
     if stream is None:
         return make(shape, dtype=dtype, device=device)
     if not isinstance(stream, torch.cuda.Stream):  # a handle; 0 is the default stream, of which ExternalStream makes a new one
@@ -622,9 +628,9 @@ def nq_kv_plan(cached_lens, new_lens, block_table, free_pages, free_head, tokens
     width, ld = _table(block_table, B)
     _need(tokens >= 0, "tokens must not be negative")
     # One allocation for the int32 results.
-    buf = torch.empty(2 * B + 2 + tokens, dtype=_i32, device=new_lens.device)
+    buf = _new(torch.empty, 2 * B + 2 + tokens, _i32, new_lens.device, stream)
     cu_q, kv_lens, head_out, positions = buf.split_with_sizes((B + 1, B, 1, tokens))
-    slots = torch.empty(tokens, dtype=_i64, device=new_lens.device)
+    slots = _new(torch.empty, tokens, _i64, new_lens.device, stream)
     if free_head_out is None:
         free_head_out = head_out
     elif _device_of(free_head_out) != dev or free_head_out.dtype is not _i32 or free_head_out.shape != (1,):
@@ -683,13 +689,13 @@ def nq_kv_gather_nvfp4(cache, slots, k_scale, v_scale, head_dim: int, *, k_out=N
     kt = vt = H * head_dim
     kh = vh = head_dim
     if k_out is None:
-        k_out = torch.empty(shape, dtype=_bf16, device=cache.device)
+        k_out = _new(torch.empty, shape, _bf16, cache.device, stream)
     else:
         if _device_of(k_out) != dev or k_out.dtype is not _bf16 or k_out.shape != shape:
             _wrong(dev, k_out=(k_out, _bf16, shape, False))
         kt, kh = _heads(k_out, "k_out")
     if v_out is None:
-        v_out = torch.empty(shape, dtype=_bf16, device=cache.device)
+        v_out = _new(torch.empty, shape, _bf16, cache.device, stream)
     else:
         if _device_of(v_out) != dev or v_out.dtype is not _bf16 or v_out.shape != shape:
             _wrong(dev, v_out=(v_out, _bf16, shape, False))
@@ -737,14 +743,14 @@ def nq_attention_nvfp4_kv(q, cache, block_table, kv_lens, cu_q, k_scale, v_scale
     pages, H, page, stride = _cache(cache, d)
     width, ld = _table(block_table, B)
     if out is None:
-        out = torch.empty((T, heads, d), dtype=_bf16, device=q.device)
+        out = _new(torch.empty, (T, heads, d), _bf16, q.device, stream)
         ot, oh = heads * d, d
     else:
         if _device_of(out) != dev or out.dtype is not _bf16 or out.shape != q.shape:
             _wrong(dev, out=(out, _bf16, (T, heads, d), False))
         ot, oh = _heads(out, "out")
     if want_lse and lse is None:
-        lse = torch.empty((T, heads), dtype=_f32, device=q.device)
+        lse = _new(torch.empty, (T, heads), _f32, q.device, stream)
     lse_p, ld_lse = None, heads
     if lse is not None:
         if _device_of(lse) != dev or lse.dtype is not _f32 or lse.shape != (T, heads):

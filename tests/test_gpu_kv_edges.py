@@ -164,3 +164,30 @@ def test_a_workspace_of_the_default_stream(nq, monkeypatch):
             assert made.pop() == (side.cuda_stream if handle in (side, side.cuda_stream) else 0) and not made
             torch.cuda.synchronize()
             assert torch.equal(out, want) and torch.equal(lse, want_lse)
+
+
+def test_results_belong_to_the_stream_of_the_call(nq):
+    """The current stream still writes to memory that it has given back when a call on another stream makes its results."""
+    D, page = 128, 16
+    s = make(nq, [1] * 6, [900] * 6, 8, 2, D, page, seed=14)
+    table, lens, head = s["table"].clone(), i32([900] * 6), i32([0])
+    free = torch.arange(40, dtype=torch.int32, device="cuda")
+    slots = torch.arange(2000, device="cuda")
+
+    def results(**on):
+        out = call(nq, s, want_lse=True, **on)
+        kv = nq.nq_kv_gather_nvfp4(s["cache"], slots, s["gk"], s["gv"], D, **on)
+        return *out, *kv, *nq.nq_kv_plan(lens, i32_one, table, free, head, 6, page, **on)
+    i32_one = i32([1] * 6)
+    want = results()
+    side = torch.cuda.Stream()
+    for handle in (side, side.cuda_stream):
+        torch.cuda.synchronize()
+        torch.cuda._sleep(1 << 28)
+        old = [torch.full_like(w, 77) for w in want for _ in range(2)]
+        del old  # its memory is the current stream's again, and the fills are still to come
+        got = results(stream=handle)
+        torch.cuda.synchronize()
+        for g, w in zip(got, want):
+            assert torch.equal(torch.nan_to_num(g.float(), nan=7e9), torch.nan_to_num(w.float(), nan=7e9))
+    nq.nq_check_device_errors()
