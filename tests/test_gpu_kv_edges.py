@@ -1,9 +1,11 @@
-"""GPU tests of the 4-bit key/value cache at its edges."""
+"""GPU tests of the 4-bit key/value cache at its edges: rows and requests without keys among others, weights far below
+the largest, scales and queries of extreme size, lengths that do not fit, streams, and every form of the kernels."""
 import numpy as np
 import pytest
 import torch
 
 import kv_helpers as K
+from gpu_helpers import Guarded
 from test_gpu_kv import check, f32, i32, make, nq  # noqa: F401  (fixture)
 
 pytestmark = pytest.mark.gpu
@@ -190,4 +192,104 @@ def test_results_belong_to_the_stream_of_the_call(nq):
         torch.cuda.synchronize()
         for g, w in zip(got, want):
             assert torch.equal(torch.nan_to_num(g.float(), nan=7e9), torch.nan_to_num(w.float(), nan=7e9))
+    nq.nq_check_device_errors()
+
+
+# -------------------------------------------------------------- every form of the kernel for few rows, many requests ----
+# (query heads, kv heads, D, new tokens at most): 4 to 60 rows a request and kv head, and so one to four row tiles of a
+# warp, one to three tiles a request
+WALKS = [(8, 2, 64, 1), (8, 2, 64, 3), (8, 2, 64, 6), (8, 2, 64, 11), (12, 2, 64, 10), (8, 2, 128, 3), (8, 2, 128, 7),
+         (8, 2, 128, 11), (4, 2, 256, 4), (4, 2, 256, 6), (8, 2, 256, 6)]
+
+
+def ragged(nq, heads, kv_heads, D, most, B=150, least=0, seed=0):
+    """B requests of 0 ... `most` new tokens (two thirds of them of `most`) and of lengths from `least` on."""
+    rng = np.random.default_rng(seed + D + most)
+    n = [most if x else int(rng.integers(0, most + 1)) for x in rng.random(B) < 0.67]
+    t = [max(least, int(x)) for x in rng.integers(0, 500, B)]
+    t[:4] = [1, 16, 17, 1500]
+    return make(nq, n, t, heads, kv_heads, D, 16, seed=seed, tail=3)
+
+
+@pytest.mark.parametrize("heads,kv_heads,D,most", WALKS)
+@pytest.mark.parametrize("window,causal", [(0, True), (90, True), (0, False), (200, False), (1, True)])
+def test_many_requests_of_few_rows(nq, heads, kv_heads, D, most, window, causal):
+    check(nq, ragged(nq, heads, kv_heads, D, most), window=window, causal=causal)
+
+
+@pytest.mark.parametrize("heads,kv_heads,D,most", WALKS)
+def test_many_requests_at_any_address(nq, heads, kv_heads, D, most):
+    s = ragged(nq, heads, kv_heads, D, most, seed=1)
+    T, H, rows = s["q"].shape[0], heads, sum(s["n"])
+    want, want_lse = call(nq, s, want_lse=True)
+    raw = torch.full((T * (H * D + 3) + 5,), 9.0, dtype=torch.bfloat16, device="cuda")
+    odd = raw[5:].view(T, H * D + 3)[:, :H * D].view(T, H, D)  # rows that start off every alignment
+    odd.copy_(s["q"])
+    out = Guarded(T, H * D, torch.bfloat16, pad=5)
+    lse = torch.full((T, H + 3), 9.0, device="cuda")
+    call(nq, {**s, "q": odd}, out=out.view.view(T, H, D), lse=lse[:, :H])
+    assert torch.equal(out.view.reshape(T, H, D)[:rows], want[:rows]) and out.guards_intact()
+    assert torch.equal(lse[:rows, :H], want_lse[:rows]) and bool((lse[:, H:] == 9.0).all()) and bool((lse[rows:] == 9.0).all())
+    out = torch.empty((H, T, D), dtype=torch.bfloat16, device="cuda").transpose(0, 1)
+    call(nq, {**s, "q": s["q"].transpose(0, 1).contiguous().transpose(0, 1)}, out=out)
+    assert torch.equal(out[:rows], want[:rows])
+
+
+@pytest.mark.parametrize("heads,kv_heads,D,most", WALKS)
+def test_many_requests_with_pages_outside_the_cache(nq, heads, kv_heads, D, most):
+    """First, middle and last pages without a page in the cache: as if their keys were not there (all keys in sight)."""
+    s = ragged(nq, heads, kv_heads, D, most, least=60, seed=2)
+    rng = np.random.default_rng(3)
+    bad, rest, left = s["table"].clone(), torch.full_like(s["table"], 1 << 30), []
+    for b, t in enumerate(s["t"]):
+        pages = -(-t // 16)
+        gone = {0: [], 1: [0], 2: [pages - 1], 3: sorted({0, pages // 3, pages // 2}), 4: list(range(pages)),
+                5: sorted(rng.permutation(pages)[:pages // 2].tolist())}[b % 6]
+        keep = [p for p in range(pages) if p not in gone]
+        for p in gone:
+            bad[b, p] = [-1, s["cache"].shape[0], 1 << 30][p % 3]
+        rest[b, :len(keep)] = s["table"][b, keep]
+        left.append(t - sum(min(16, t - 16 * p) for p in gone))
+    out, lse = call(nq, {**s, "table": bad}, want_lse=True, flags=nq.FLAG_NONCAUSAL)
+    with pytest.raises(nq.NQError, match="bit 2"):
+        nq.nq_check_device_errors()
+    k, v = K.decode(s["cache"], D, 16)
+    o, l, tol, tol_lse = K.attention(s["q"], k, v, float(s["gk"]), float(s["gv"]), rest, left, s["cu"].tolist(), 16, D**-0.5,
+                                     causal=False)
+    rows = sum(s["n"])
+    assert bool(((out[:rows].double() - o[:rows]).abs() <= tol[:rows]).all())
+    empty = torch.isneginf(l[:rows])
+    assert bool(empty.any()) and torch.equal(torch.isneginf(lse[:rows]), empty)
+    assert bool((torch.where(empty, 0.0, (lse[:rows].double() - l[:rows]).abs()) <= tol_lse[:rows]).all())
+
+
+# ------------------------------------------------------------------------------------------ groups and empty requests ----
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("group,kv_heads", [(3, 2), (7, 1), (33, 1), (129, 1), (1024, 1)])
+@pytest.mark.parametrize("B", [3, 40, 300])
+def test_groups_of_any_size_among_empty_requests(nq, D, group, kv_heads, B):
+    """Three requests that have rows; the others hold keys only, as those of a padded batch (which makes the average of
+    rows small, and so sends groups of up to 1024 heads to the kernel for few rows)."""
+    n, t = [0] * B, [5 + b % 40 for b in range(B)]
+    for b, (m, x) in zip((0, B // 2, B - 1), ((2, 300), (1, 77), (3, 2))):
+        n[b], t[b] = m, x
+    s = make(nq, n, t, group * kv_heads, kv_heads, D, 16, seed=group, tail=2)
+    check(nq, s)
+    check(nq, s, window=20)
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_rows_before_the_first_request_are_left(nq, form, D):
+    s = make(nq, *FORMS[form], 8, 2, D, 16, seed=21)
+    want, want_lse = call(nq, s, want_lse=True)
+    q = torch.cat([torch.full_like(s["q"][:3], float("nan")), s["q"]])
+    out, lse = torch.full_like(q, 123.0), torch.full(q.shape[:2], 123.0, device="cuda")
+    call(nq, {**s, "q": q, "cu": s["cu"] + 3}, out=out, lse=lse)
+    assert bool((out[:3] == 123.0).all()) and bool((lse[:3] == 123.0).all())
+    if form == "chunks":  # the same parts; elsewhere rows and parts fall differently
+        assert torch.equal(out[3:], want) and torch.equal(lse[3:], want_lse)
+    o, l, tol, tol_lse = K.attention(s["q"], *K.decode(s["cache"], D, 16), float(s["gk"]), float(s["gv"]), s["table"], s["t"],
+                                     s["cu"].tolist(), 16, D**-0.5)
+    assert bool(((out[3:].double() - o).abs() <= tol).all()) and bool(((lse[3:].double() - l).abs() <= tol_lse).all())
     nq.nq_check_device_errors()
