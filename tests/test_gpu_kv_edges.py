@@ -293,3 +293,20 @@ def test_rows_before_the_first_request_are_left(nq, form, D):
                                      s["cu"].tolist(), 16, D**-0.5)
     assert bool(((out[3:].double() - o).abs() <= tol).all()) and bool(((lse[3:].double() - l).abs() <= tol_lse).all())
     nq.nq_check_device_errors()
+
+
+# ---------------------------------------------------------------------------------------------------- the binding ----
+def test_scales_of_one_element_in_any_shape(nq):
+    s = make(nq, [1, 2], [20, 40], 4, 2, 128, 16, seed=22)
+    want, _ = call(nq, s)
+    slots = torch.arange(32, device="cuda")
+    back = nq.nq_kv_gather_nvfp4(s["cache"], slots, s["gk"], s["gv"], 128)
+    cache, again = torch.zeros_like(s["cache"]), torch.zeros_like(s["cache"])
+    nq.nq_kv_append_nvfp4(*back, slots, cache, s["gk"], s["gv"])
+    for shape in ((), (1, 1), (1, 1, 1)):
+        gk, gv = s["gk"].reshape(shape), s["gv"].reshape(shape)
+        assert torch.equal(call(nq, {**s, "gk": gk, "gv": gv})[0], want)
+        got = nq.nq_kv_gather_nvfp4(s["cache"], slots, gk, gv, 128)
+        assert all(torch.equal(a.view(torch.int16), b.view(torch.int16)) for a, b in zip(got, back))
+        nq.nq_kv_append_nvfp4(*back, slots, again.zero_(), gk, gv)
+        assert torch.equal(again, cache)
