@@ -9,9 +9,8 @@ passed in has to be ready.  (Then the key/value cache calls make their results
 on that stream; the norm and quantization calls take theirs from the current
 stream's memory, so pass outputs of your own or order the two streams.)  Every
 arithmetic step runs in the library's CUDA kernels; there is no CPU or PyTorch
-fallback.  The library is loaded on first
-use, and that use raises ImportError when it has not been built
-(``python -m fp4_activation_quantization_b200.build``).
+fallback.  The library is loaded on first use, and that use raises ImportError
+when it has not been built (``python -m fp4_activation_quantization_b200.build``).
 
 Functions carry the C names:
 ``nq_fused_add_rmsnorm_quant_fp8``, ``nq_rmsnorm_quant_fp8_static``,
@@ -158,7 +157,8 @@ def nq_selftest_division(divisors, a_bits_begin: int = 0, count: int = 1 << 32, 
 def nq_check_device_errors() -> None:
     """Raise NQError if a kernel recorded an error since the last check (a MoE
     destination row out of range; a key/value slot or page out of range, a plan
-    that ran out of pages).  Synchronous: waits for every stream of the
+    that ran out of pages, table columns or token rows, a bounded wait of an
+    attention kernel that ran out).  Synchronous: waits for every stream of the
     current device, then reads and clears the device error word atomically."""
     _check(_get_lib().nq_check_device_errors(), "nq_check_device_errors")
 

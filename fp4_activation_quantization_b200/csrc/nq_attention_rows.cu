@@ -22,9 +22,11 @@
 // Work.  S^T = K' q^T and O^T = V'^T P^T put the 16 tokens (or dimensions) on
 // the 16-row side of the product and up to 8 rows of a (request, kv head) on
 // its 8-column side.  An atom of D = 128 (2304 bytes) costs a warp scheduler about
-// 405 cycles: the conversion of its codes and the products share the issue slots,
-// which binds before HBM does (128 ragged requests to 8192 keys, 8 kv heads: 154 us,
-// 0.66 of copy bandwidth; 2 requests of 131071 keys 72 us, 0.64).
+// 405 cycles: the conversion of its codes and the products share the issue slots
+// (61 % of them used), and each warp's chain of scores, vote, weights and values,
+// with 3.5 warps a scheduler to cover it, binds before HBM does (128 ragged requests
+// to 8192 keys, 8 kv heads: 154 us, 0.66 of copy bandwidth; 2 requests of 131071
+// keys 72 us, 0.64).
 //
 // Split.  The atoms of all (request, row tile, kv head) segments form one axis,
 // which is shared out equally whatever the lengths, in one of two ways:
@@ -35,7 +37,7 @@
 //    go to the workspace, and a second launch, which starts under the first
 //    one's end, joins them.
 //  - few segments: every CTA takes one chunk of one segment, of 32 atoms or more,
-//    its warps a quarter each; they are joined in shared memory, and the CTA
+//    its warps an eighth each; they are joined in shared memory, and the CTA
 //    that arrives last at a segment's counter joins its chunks.  One launch: a
 //    second one costs as much as a short context takes.
 // Parts are joined in the order of the tokens, so results do not depend on
@@ -261,7 +263,8 @@ struct Join {
 
 // CTAs of an SM (of 4 warps; of the chunks' 8, half as many).  128 x 16 rows at
 // three instead of two spilled 500 bytes a thread: 24 x 16 rows over 4096 keys 71
-// us, was 58.
+// us, was 58.  (Chunks of 256 x 16 rows spill 534 bytes; as twice 8 rows each key
+// is converted twice: 4 requests 42 us, with the spills 28.7.)
 template <int D, int NT, bool WALK>
 __global__ void __launch_bounds__((WALK ? kWalkWarps : kChunkWarps) * 32,
                                   (NT == 1 && D < 256 ? 4 : (NT == 2 && D == 64 ? 3 : 2)) * kWalkWarps / (WALK ? kWalkWarps : kChunkWarps))
@@ -865,7 +868,7 @@ __global__ void __launch_bounds__((WALK ? kWalkWarps : kChunkWarps) * 32,
       }
       u = seg0 + ub;
     } else {
-      // The four warps' quarters of the chunk, through shared memory (over the rings).
+      // The warps' shares of the chunk, through shared memory (over the rings).
       float* res = reinterpret_cast<float*>(smem);  // [kWarps][R][kPitch]
       float* stat = res + kWarps * R * kPitch;      // [kWarps][R][2]
       __syncthreads();

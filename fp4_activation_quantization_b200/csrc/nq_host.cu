@@ -17,8 +17,9 @@
 #include "nq_internal.h"
 
 // Device error word of this library: bit 1 is set by a MoE dispatch whose
-// destination row was out of range, bits 2 and 3 by the key/value cache calls
-// (nq_kv.h); read and cleared by nq_check_device_errors.  A symbol, not an allocation; one per device.
+// destination row was out of range, bits 2, 3 and 4 by the key/value cache calls
+// and attention (nq_kv.h); read and cleared by nq_check_device_errors.  A symbol,
+// not an allocation; one per device.
 __device__ uint32_t g_nq_device_error;
 // Where take_error_word leaves the word it cleared, for the host to read.
 __device__ uint32_t g_nq_device_error_taken;

@@ -170,8 +170,8 @@ const char* nq_status_string(nq_status status);
  * outside the key/value cache (bit 2: skipped), a key/value plan ran out of
  * pages, table columns or token rows (bit 3), a bounded wait of an attention
  * kernel ran out (bit 4: its output is not valid), or if the device reported an
- * error while synchronizing.  Kernels never trap or hang: the attention kernel
- * for prompts alone waits, on its own CTA's barriers, each time with a limit. */
+ * error while synchronizing.  Kernels never trap or hang: both attention kernels
+ * wait on their own CTA's barriers, each time with a limit, the others never. */
 nq_status nq_check_device_errors(void);
 /* Diagnostic (tests): checks, on the device, the bounded division the dynamic
  * FP8 path uses for RN(y / s) (a correctly rounded reciprocal r = RN(1 / s),
