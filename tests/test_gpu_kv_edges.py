@@ -310,3 +310,74 @@ def test_scales_of_one_element_in_any_shape(nq):
         assert all(torch.equal(a.view(torch.int16), b.view(torch.int16)) for a, b in zip(got, back))
         nq.nq_kv_append_nvfp4(*back, slots, again.zero_(), gk, gv)
         assert torch.equal(again, cache)
+
+
+# ------------------------------------------------------------------------------------------- calls beside one another ----
+def test_calls_at_the_same_time(nq):
+    """Every form of the kernels on four streams at once, a workspace each: the bits that each gives alone."""
+    batches = [make(nq, *FORMS[f], 8, 2, D, 16, seed=23) for D in (64, 128, 256) for f in FORMS]
+    batches += [make(nq, [400] * 6, [700 + 60 * i for i in range(6)], 16, 4, D, 64, seed=24) for D in (128, 256)]
+    want = [call(nq, s, want_lse=True) for s in batches]
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    spaces = [torch.zeros(nq.ATTENTION_WORKSPACE_BYTES, dtype=torch.uint8, device="cuda") for _ in streams]
+    outs = [[tuple(torch.empty_like(x) for x in w) for w in want] for _ in streams]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for i in range(len(batches)):
+            for j, stream in enumerate(streams):
+                k = (i + 3 * j) % len(batches)
+                call(nq, batches[k], out=outs[j][k][0], lse=outs[j][k][1], workspace=spaces[j], stream=stream)
+        torch.cuda.synchronize()
+        for got in outs:
+            for (o, l), (ow, lw) in zip(got, want):
+                assert torch.equal(o, ow) and torch.equal(l, lw)
+                o.fill_(9.0)
+                l.fill_(9.0)
+        torch.cuda.synchronize()
+    nq.nq_check_device_errors()
+
+
+@pytest.mark.parametrize("new", [[1] * 40, [3, 0, 90] * 4, [150, 1]])
+def test_a_step_whose_launches_overlap(nq, new):
+    """Plan, append, attention and gather, each of which may start while the one before ends, captured and replayed."""
+    H, G, D, page, B = 2, 4, 128, 16, len(new)
+    T = sum(new) + 3
+    gen = torch.Generator("cuda").manual_seed(B)
+    gk = f32(4.6 / 2688)
+    qkv = torch.randn((T, H * G + 2 * H, D), generator=gen, device="cuda").bfloat16()
+    q, k, v = qkv.split_with_sizes((H * G, H, H), 1)
+    steps, pages = 6, 6 * sum(new) + B
+    free = torch.randperm(pages, generator=gen, device="cuda").to(torch.int32)
+    ws = torch.zeros(nq.ATTENTION_WORKSPACE_BYTES, dtype=torch.uint8, device="cuda")
+
+    def server():
+        return dict(cache=torch.zeros(nq.kv_cache_shape(pages, H, D, page), dtype=torch.uint8, device="cuda"),
+                    table=torch.full((B, -(-steps * max(new) // page)), -1, dtype=torch.int32, device="cuda"), head=i32([0]),
+                    lens=i32([0] * B))
+
+    def step(s, flags):
+        cu, lens, _, slots, _ = nq.nq_kv_plan(s["lens"], i_new, s["table"], free, s["head"], T, page, free_head_out=s["head"],
+                                              flags=flags)
+        nq.nq_kv_append_nvfp4(k, v, slots, s["cache"], gk, gk, flags=flags)
+        out, _ = nq.nq_attention_nvfp4_kv(q, s["cache"], s["table"], lens, cu, gk, gk, workspace=ws, flags=flags,
+                                          out=s.setdefault("out", torch.zeros_like(q)))
+        back = nq.nq_kv_gather_nvfp4(s["cache"], slots, gk, gk, D, flags=flags)
+        s["lens"].copy_(lens)
+        return out, *back
+    i_new = i32(new)
+    plain, graphed = server(), server()
+    step({**server()}, nq.FLAG_PDL)  # everything is loaded before the capture
+    graph, stream = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    graphed["out"] = torch.zeros_like(q)
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=stream):
+        got = step(graphed, nq.FLAG_PDL)
+    for _ in range(steps):
+        graph.replay()
+        want = step(plain, 0)
+        for name in ("cache", "table", "head", "lens"):
+            assert torch.equal(plain[name], graphed[name]), name
+        for g, w in zip(got, want):
+            assert torch.equal(g, w)
+    assert plain["lens"].tolist() == [steps * n for n in new]
+    nq.nq_check_device_errors()
