@@ -428,8 +428,10 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
       const Item& it = s_item[k & 1];  // read again where it is used: the block loop needs the registers
       const int n = it.blocks;
       if (it.rows <= 128 * t) continue;
-      float c;
-      {
+      float c = 0.0f;
+      // Without keys no queries are laid out and q_full does not count: nothing but o_last holds these warps to the
+      // products' pace, so they could pass two of its phases, which one parity cannot tell apart.
+      if (n > 0) {
         // The row, scaled by a power of two (and the score factor's sign), as f16.
         const bool live = row < it.rows;
         const int x = it.row0 + row, token = x / a.group;
@@ -874,18 +876,13 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const AttnArgs a) {
         const int n = s_item[item & 1].blocks, tiles = s_item[item & 1].rows > 128 ? 2 : 1;
         leave(item);
         const uint32_t both = uint32_t(tiles) | 1u;  // bit t: tile t has rows
+        if (n == 0) continue;  // no barrier but the item's own takes part in it
         const uint32_t q_now = q_par;
         q_par ^= both;
         auto wait_q = [&](int t) {
           ok = ok && mbar_wait_warp(q_full(t), (q_now >> t) & 1, gave_up);
           fence_after();
         };
-        if (n == 0) {
-          // No phase of q_full is passed by: the softmax warps may be an item behind, and the parity of the next
-          // item's phase is that of the one before this.
-          for (int t = 0; t < tiles; ++t) wait_q(t);
-          continue;
-        }
         wait_slot(q);
         if constexpr (C::kTiles == 2) {
           for (int t = 0; t < tiles && ok; ++t) {

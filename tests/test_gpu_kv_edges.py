@@ -15,6 +15,20 @@ def call(nq, s, **more):
     return nq.nq_attention_nvfp4_kv(s["q"], s["cache"], s["table"], s["kv_lens"], s["cu"], s["gk"], s["gv"], **more)
 
 
+@pytest.mark.parametrize("heads,kv_heads,D", [(16, 1, 64), (16, 2, 128), (8, 2, 256)])
+@pytest.mark.parametrize("seed", range(4))
+def test_runs_of_tiles_without_keys(nq, heads, kv_heads, D, seed):
+    """Most requests without keys, of every number of rows: a CTA takes several tiles without keys one after another."""
+    rng = np.random.default_rng(seed)
+    n = [int(x) for x in rng.integers(1, 180, 120)]
+    t = [int(x) for x in rng.choice([0, 0, 0, 0, 1, 5, 300], 120)]
+    s = make(nq, n, t, heads, kv_heads, D, 16, seed=seed, tail=1)
+    ws = torch.zeros(nq.ATTENTION_WORKSPACE_BYTES, dtype=torch.uint8, device="cuda")
+    for causal in (False, True):
+        for _ in range(5):
+            check(nq, s, causal=causal, workspace=ws)
+
+
 # Rows and keys of a batch that takes each form of the kernels: one chunk a CTA, a share a warp, 128-row tiles.
 FORMS = {"chunks": ([1] * 3, [700, 40, 300]), "walk": ([1] * 300, [100 + 7 * (i % 50) for i in range(300)]),
          "tiles": ([150, 200], [300, 200])}
